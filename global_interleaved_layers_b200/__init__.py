@@ -40,6 +40,11 @@ ERR_LAUNCH = -5
 ERR_TIMEOUT = -6
 ERR_DEVICE = -7
 ERR_SEQLEN = -8
+ERR_PAGE = -9
+PAGES_BF16 = 0
+PAGES_E4M3 = 1
+PROBS_F32 = 0
+PROBS_BF16 = 1
 
 
 class GemmaAttnParams(ctypes.Structure):
@@ -47,6 +52,12 @@ class GemmaAttnParams(ctypes.Structure):
                 ("rope_base", ctypes.c_float), ("softmax_scale", ctypes.c_float),
                 ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32)]
+
+
+class GemmaAttnPagedCache(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class GemmaAttnError(RuntimeError):
@@ -74,6 +85,12 @@ _lib.gemma_attn_tile_plan.argtypes = [_I, _I, _P, _I, _I, _I, _P, ctypes.c_int64
 _lib.gemma_attn_decode_noalloc.argtypes = [_PP, _P, _P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P]
 _lib.gemma_attn_cache_append.argtypes = [_PP, _P, _P, _P, _P, _I, _I, _P, _I, _I, _P]
 _lib.gemma_attn_decode_shard.argtypes = [_PP, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _I, _P]
+_PC = ctypes.POINTER(GemmaAttnPagedCache)
+_lib.gemma_attn_paged_append.argtypes = [_PP, _PC, _P, _P, _P, _P, _I, _I, _P]
+_lib.gemma_attn_paged_gather.argtypes = [_PP, _PC, _P, _P, _P, _P, _I, _I, _P]
+_lib.gemma_attn_paged_workspace_size.argtypes = [_PP, _PC, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]
+_lib.gemma_attn_paged_attend.argtypes = [_PP, _PC, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, ctypes.c_size_t, _P]
+_lib.gemma_attn_draft_verify.argtypes = [_P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P]
 _lib.gemma_attn_check.argtypes = [_P]
 _lib.gemma_attn_selftest_umma.argtypes = [_I, _P, _P, _P, _P, _P]
 _lib.gemma_attn_selftest_timeout.argtypes = [_P, _P]
@@ -81,7 +98,9 @@ for _f in ("gemma_attn_prefill_workspace_size", "gemma_attn_prefill", "gemma_att
            "gemma_attn_decode_num_splits", "gemma_attn_combine", "gemma_attn_tile_plan", "gemma_attn_check",
            "gemma_attn_selftest_umma", "gemma_attn_decode_noalloc", "gemma_attn_selftest_timeout",
            "gemma_attn_cache_append", "gemma_attn_decode_shard",
-           "gemma_attn_prefill_rotate", "gemma_attn_prefill_attend"):
+           "gemma_attn_prefill_rotate", "gemma_attn_prefill_attend", "gemma_attn_paged_append",
+           "gemma_attn_paged_gather", "gemma_attn_paged_workspace_size", "gemma_attn_paged_attend",
+           "gemma_attn_draft_verify"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 
@@ -227,6 +246,168 @@ def gemma_attn_tile_plan(kind: int, window: int, cu_seqlens_host, bm: int, bn: i
     _check(_lib.gemma_attn_tile_plan(kind, window, _ptr(cu), cu.shape[0] - 1, bm, bn, _ptr(out), n.value,
                                      ctypes.byref(n)), "gemma_attn_tile_plan")
     return out[: int(n.value)]
+
+
+def _require(cond: bool, where: str, what: str) -> None:
+    if not cond:
+        e = GemmaAttnError(ERR_INVALID_ARG, where)
+        e.args = (f"{e.args[0]}: {what}",)
+        raise e
+
+
+def _tensor(x, where: str, name: str, dtypes, shape=None, device=None):
+    """A torch tensor argument of a paged-cache or draft call: type, shape, layout and device are
+    checked (raw addresses and None pass)."""
+    if x is None or isinstance(x, int):
+        return x
+    _require(x.dtype in dtypes, where, f"{name} is {x.dtype}")
+    _require(x.is_contiguous(), where, f"{name} is not contiguous")
+    _require(shape is None or tuple(x.shape) == shape, where, f"{name} has shape {tuple(x.shape)}, not {shape}")
+    _require(device is None or x.device == device, where, f"{name} is on {x.device}, not {device}")
+    return x.data_ptr()
+
+
+def paged_cache(k_pages, v_pages, block_table, k_scales=None, v_scales=None) -> GemmaAttnPagedCache:
+    """Handle of a paged cache over torch tensors, which it keeps alive: k_pages (and v_pages; None for
+    global layers) [num_pages, kv_heads, page_size, head_dim] in bfloat16 or float8_e4m3fn, the latter
+    with float32 scales [num_pages, kv_heads, page_size]; block_table [batch, max_blocks] int32."""
+    import torch
+    where = "paged_cache"
+    _require(k_pages.dim() == 4 and block_table.dim() == 2, where, "k_pages has 4 dimensions, block_table 2")
+    e4m3 = k_pages.dtype == torch.float8_e4m3fn
+    dev, shape = k_pages.device, tuple(k_pages.shape)
+    k = _tensor(k_pages, where, "k_pages", (torch.bfloat16, torch.float8_e4m3fn))
+    v = _tensor(v_pages, where, "v_pages", (k_pages.dtype,), shape, dev)
+    _require(e4m3 == (k_scales is not None) and (e4m3 and v_pages is not None) == (v_scales is not None), where,
+             "float8_e4m3fn pages have scales, bfloat16 pages none")
+    ks = _tensor(k_scales, where, "k_scales", (torch.float32,), shape[:3], dev)
+    vs = _tensor(v_scales, where, "v_scales", (torch.float32,), shape[:3], dev)
+    tab = _tensor(block_table, where, "block_table", (torch.int32,), None, dev)
+    c = GemmaAttnPagedCache(k, v, ks, vs, tab, shape[0], shape[2], block_table.shape[1],
+                            PAGES_E4M3 if e4m3 else PAGES_BF16)
+    c.tensors = (k_pages, v_pages, block_table, k_scales, v_scales)
+    return c
+
+
+class _On:
+    """The device of a call's tensors made current, and the stream to launch on (by default that
+    device's current one)."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.old = device, stream, None
+
+    def __enter__(self):
+        import torch
+        if self.device is not None and self.device.type == "cuda":
+            now = torch.cuda.current_device()
+            if now != self.device.index:
+                self.old = now
+                torch.cuda.set_device(self.device)
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.old is not None:
+            import torch
+            torch.cuda.set_device(self.old)
+
+
+def _cache_fits(p: GemmaAttnParams, cache: GemmaAttnPagedCache, batch: int, where: str):
+    """The handle's tensors (when it was made from tensors) against the layer; returns their device."""
+    tensors = getattr(cache, "tensors", None)
+    if tensors is None:
+        return None
+    kp, _, table = tensors[:3]
+    _require(kp.shape[1] == p.num_kv_heads and kp.shape[3] == p.head_dim, where,
+             f"k_pages has {kp.shape[1]} heads of {kp.shape[3]} dims, the layer {p.num_kv_heads} of {p.head_dim}")
+    _require(table.shape[0] >= batch, where, f"block_table has {table.shape[0]} rows for {batch} sequences")
+    return kp.device
+
+
+def gemma_attn_paged_append(p: GemmaAttnParams, cache: GemmaAttnPagedCache, new_k, new_v, cu_q, cache_seqlens,
+                            batch: int, total_q: int, stream=None) -> None:
+    """New rows into a paged cache: row cu_q[b] + i goes to position cache_seqlens[b] + i of sequence b."""
+    import torch
+    where = "gemma_attn_paged_append"
+    dev = _cache_fits(p, cache, batch, where)
+    shape = (total_q, p.num_kv_heads, p.head_dim)
+    k = _tensor(new_k, where, "new_k", (torch.bfloat16,), shape, dev)
+    v = _tensor(new_v, where, "new_v", (torch.bfloat16,), shape, dev)
+    cu = _tensor(cu_q, where, "cu_q", (torch.int32,), (batch + 1,), dev)
+    lens = _tensor(cache_seqlens, where, "cache_seqlens", (torch.int32,), (batch,), dev)
+    with _On(dev, stream) as st:
+        _check(_lib.gemma_attn_paged_append(ctypes.byref(p), ctypes.byref(cache), k, v, cu, lens, batch, total_q, st),
+               where)
+
+
+def gemma_attn_paged_gather(p: GemmaAttnParams, cache: GemmaAttnPagedCache, starts, cu_out, out_k, out_v, batch: int,
+                            total_out: int, stream=None) -> None:
+    """Rows read back: row cu_out[b] + i receives position starts[b] + i of sequence b (params' out_dtype)."""
+    import torch
+    where = "gemma_attn_paged_gather"
+    dev = _cache_fits(p, cache, batch, where)
+    shape = (total_out, p.num_kv_heads, p.head_dim)
+    dt = (torch.float32 if p.out_dtype == OUT_F32 else torch.bfloat16,)
+    k = _tensor(out_k, where, "out_k", dt, shape, dev)
+    v = _tensor(out_v, where, "out_v", dt, shape, dev)
+    first = _tensor(starts, where, "starts", (torch.int32,), (batch,), dev)
+    cu = _tensor(cu_out, where, "cu_out", (torch.int32,), (batch + 1,), dev)
+    with _On(dev, stream) as st:
+        _check(_lib.gemma_attn_paged_gather(ctypes.byref(p), ctypes.byref(cache), first, cu, k, v, batch, total_out, st),
+               where)
+
+
+def gemma_attn_paged_workspace_size(p: GemmaAttnParams, cache: GemmaAttnPagedCache, batch: int, total_q: int,
+                                    max_q: int, max_cache_len: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.gemma_attn_paged_workspace_size(ctypes.byref(p), ctypes.byref(cache), batch, total_q, max_q,
+                                                max_cache_len, ctypes.byref(n)), "gemma_attn_paged_workspace_size")
+    return int(n.value)
+
+
+def gemma_attn_paged_attend(p: GemmaAttnParams, cache: GemmaAttnPagedCache, q, cu_q, cache_seqlens, out, lse,
+                            batch: int, total_q: int, max_q: int, max_cache_len: int, workspace, workspace_bytes: int,
+                            stream=None) -> None:
+    """Attention of a chunk of new tokens over a paged cache that already holds their rows."""
+    import torch
+    where = "gemma_attn_paged_attend"
+    dev = _cache_fits(p, cache, batch, where)
+    shape = (total_q, p.num_q_heads, p.head_dim)
+    qp = _tensor(q, where, "q", (torch.bfloat16,), shape, dev)
+    o = _tensor(out, where, "out", (torch.float32 if p.out_dtype == OUT_F32 else torch.bfloat16,), shape, dev)
+    ls = _tensor(lse, where, "lse", (torch.float32,), shape[:2], dev)
+    cu = _tensor(cu_q, where, "cu_q", (torch.int32,), (batch + 1,), dev)
+    lens = _tensor(cache_seqlens, where, "cache_seqlens", (torch.int32,), (batch,), dev)
+    if hasattr(workspace, "data_ptr"):
+        _require(workspace.is_contiguous() and workspace.numel() * workspace.element_size() >= workspace_bytes
+                 and (dev is None or workspace.device == dev), where, "workspace is not workspace_bytes on the cache's device")
+    with _On(dev, stream) as st:
+        _check(_lib.gemma_attn_paged_attend(ctypes.byref(p), ctypes.byref(cache), qp, cu, lens, o, ls, batch, total_q,
+                                            max_q, max_cache_len, _ptr(workspace), workspace_bytes, st), where)
+
+
+def gemma_attn_draft_verify(target_probs, draft_probs, draft_tokens, draft_lens, uniforms, noise, num_accepted,
+                            out_tokens, stream=None) -> None:
+    """Drafted tokens accepted or replaced: target_probs [batch, max_draft + 1, vocab] float32 or bfloat16,
+    draft_probs [batch, max_draft, vocab] or None (certain drafts), draft_tokens [batch, max_draft] int32,
+    draft_lens [batch] int32 or None, uniforms [batch, max_draft], noise [batch, vocab] float32;
+    num_accepted [batch] and out_tokens [batch, max_draft + 1] int32 are written."""
+    import torch
+    where = "gemma_attn_draft_verify"
+    _require(target_probs.dim() == 3, where, "target_probs has 3 dimensions")
+    b, n1, v = target_probs.shape
+    _require(n1 >= 1, where, "target_probs holds max_draft + 1 rows")
+    dev, dt, i32, f32 = target_probs.device, target_probs.dtype, (torch.int32,), (torch.float32,)
+    tp = _tensor(target_probs, where, "target_probs", (torch.float32, torch.bfloat16))
+    dp = _tensor(draft_probs, where, "draft_probs", (dt,), (b, n1 - 1, v), dev)
+    tok = _tensor(draft_tokens, where, "draft_tokens", i32, (b, n1 - 1), dev)
+    lens = _tensor(draft_lens, where, "draft_lens", i32, (b,), dev)
+    uni = _tensor(uniforms, where, "uniforms", f32, (b, n1 - 1), dev)
+    nz = _tensor(noise, where, "noise", f32, (b, v), dev)
+    acc = _tensor(num_accepted, where, "num_accepted", i32, (b,), dev)
+    out = _tensor(out_tokens, where, "out_tokens", i32, (b, n1), dev)
+    with _On(dev, stream) as st:
+        _check(_lib.gemma_attn_draft_verify(tp, dp, PROBS_BF16 if dt == torch.bfloat16 else PROBS_F32, tok, lens, uni,
+                                            nz, b, n1 - 1, v, acc, out, st), where)
 
 
 def gemma_attn_check(stream=None) -> None:

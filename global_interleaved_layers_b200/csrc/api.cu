@@ -11,6 +11,7 @@
 #include "../../include/gemma_attn.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "paged.h"
 #include "tile_plan.h"
 
 namespace gattn {
@@ -198,6 +199,7 @@ const char* gemma_attn_error_string(int status) {
     case GEMMA_ATTN_ERR_TIMEOUT: return "a device-side wait ran out of time";
     case GEMMA_ATTN_ERR_DEVICE: return "CUDA error";
     case GEMMA_ATTN_ERR_SEQLEN: return "a sequence length is < 1 or exceeds max_seqlen";
+    case GEMMA_ATTN_ERR_PAGE: return "a block-table entry is outside the page pool";
     default: return "unknown status";
   }
 }
@@ -521,6 +523,7 @@ int gemma_attn_check(void* stream_) {
   if (cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) != cudaSuccess) return GEMMA_ATTN_ERR_DEVICE;
   if (status & kStatusTimeout) return GEMMA_ATTN_ERR_TIMEOUT;
   if (status & kStatusSeqlen) return GEMMA_ATTN_ERR_SEQLEN;
+  if (status & kStatusPage) return GEMMA_ATTN_ERR_PAGE;
   return GEMMA_ATTN_OK;
 }
 

@@ -7,4 +7,8 @@
 #include "decode_umma.cu"
 #include "decode_noalloc.cu"
 #include "append.cu"
+#include "paged_rows.cu"
+#include "paged_decode.cu"
+#include "draft.cu"
+#include "paged_api.cu"
 #include "selftest.cu"

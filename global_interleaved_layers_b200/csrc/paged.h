@@ -1,0 +1,110 @@
+// paged.h -- the paged KV cache as the kernels see it, and the launch interfaces of the
+// paged-cache operators and of the draft verification.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace gattn {
+
+enum : int { kStatusPage = 4 };  // device status word: a block-table entry outside the pool
+
+struct PagedCache {
+  uint8_t* k;               // [pages, Hkv, page_size, d] bf16 or e4m3
+  uint8_t* v;               // null for K=V
+  float* k_scales;          // [pages, Hkv, page_size], e4m3 only
+  float* v_scales;
+  const int32_t* table;     // [batch, max_blocks]
+  int num_pages, page_shift, max_blocks;  // page_size = 1 << page_shift
+  int hkv, d;
+};
+
+// Page of block `blk` of sequence b, or -1 (recorded) when the entry is outside the pool.
+__device__ __forceinline__ int page_of(const PagedCache& c, int b, int blk) {
+  const int pg = __ldg(c.table + (size_t)b * c.max_blocks + blk);
+  if ((unsigned)pg < (unsigned)c.num_pages) return pg;
+  atomicOr(&g_status, kStatusPage);
+  return -1;
+}
+
+// Index of (page, head, slot) among the rows of the pool.
+__device__ __forceinline__ size_t page_row(const PagedCache& c, int page, int head, int slot) {
+  return (((size_t)page * c.hkv + head) << c.page_shift) + slot;
+}
+
+// Sequence of row t: the b with cu[b] <= t < cu[b + 1] (t < cu[batch], cu[0] = 0).
+__device__ __forceinline__ int seq_of_row(const int32_t* cu, int batch, int t) {
+  int lo = 0, hi = batch;  // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(cu + mid) <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+struct PagedAppendArgs {
+  PagedCache c;
+  const uint16_t* new_k;
+  const uint16_t* new_v;
+  const int32_t* cu_q;
+  const int32_t* lens;
+  int batch, total_q;
+  int r;                    // rotated pairs of the stored keys (0 for K=V)
+  double log2_base;
+};
+template <bool E4M3>
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
+
+struct PagedGatherArgs {
+  PagedCache c;
+  const int32_t* starts;
+  const int32_t* cu_out;
+  void* out_k;
+  void* out_v;
+  int batch, total_out;
+};
+template <bool E4M3, bool F32>
+cudaError_t launch_paged_gather(const PagedGatherArgs& a, cudaStream_t stream);
+
+struct PagedAttendArgs {
+  PagedCache c;
+  const uint16_t* q;        // [T, Hq, d]
+  const int32_t* cu_q;
+  const int32_t* lens;
+  void* out;                // [T, Hq, d]
+  float* lse;               // [T, Hq] or null
+  int out_f32;
+  int batch, total_q, max_q, max_len;
+  int hq, group;            // query heads, query heads per KV head
+  int is_local, window;
+  int r;                    // rotated pairs
+  double log2_base;
+  float softmax_scale;
+  // row-group kernel: split partials
+  float* partial_o;         // [splits, T * Hq, d]
+  float* partial_lse;       // [splits, T * Hq]
+  int splits;               // most splits of a sequence's keys
+  int row_groups;           // groups of 8 rows (query, head of the KV head's group) of the longest chunk
+};
+// Split-KV attention of 8 rows per warp-set over pages (paged_decode.cu), and its merge.
+cudaError_t launch_paged_rows(const PagedAttendArgs& a, bool e4m3, cudaStream_t stream);
+int paged_rows_splits(int batch, int hkv, int row_groups, int max_keys);
+
+struct DraftArgs {
+  const void* target;
+  const void* draft;        // null: certain drafts
+  const int32_t* tokens;
+  const int32_t* lens;      // null: all max_draft
+  const float* uniforms;
+  const float* noise;
+  int32_t* accepted;
+  int32_t* out;
+  int batch, max_draft, vocab;
+};
+cudaError_t launch_draft_verify(const DraftArgs& a, bool bf16, cudaStream_t stream);
+
+}  // namespace gattn

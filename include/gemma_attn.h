@@ -78,7 +78,18 @@ enum {
   GEMMA_ATTN_ERR_LAUNCH = -5,
   GEMMA_ATTN_ERR_TIMEOUT = -6,
   GEMMA_ATTN_ERR_DEVICE = -7,
-  GEMMA_ATTN_ERR_SEQLEN = -8
+  GEMMA_ATTN_ERR_SEQLEN = -8,
+  GEMMA_ATTN_ERR_PAGE = -9 /* a block-table entry outside the page pool (paged caches) */
+};
+
+enum {
+  GEMMA_ATTN_PAGES_BF16 = 0, /* paged cache rows in bf16 */
+  GEMMA_ATTN_PAGES_E4M3 = 1  /* rows in 8 bits (e4m3) with one power-of-two fp32 scale per row and KV head */
+};
+
+enum {
+  GEMMA_ATTN_PROBS_F32 = 0, /* gemma_attn_draft_verify: probabilities in float32 */
+  GEMMA_ATTN_PROBS_BF16 = 1 /* ... or in bfloat16 */
 };
 
 enum {
@@ -299,6 +310,137 @@ int gemma_attn_combine(const float* partial_o, const float* partial_lse, int32_t
                        void* stream);
 
 /*
+ * Paged KV cache. A layer's cache is a pool of pages; page g holds page_size consecutive
+ * token positions of one sequence for every KV head. Sequence b's positions
+ * [i * page_size, (i + 1) * page_size) are in page block_table[b][i].
+ *   k_pages   [num_pages, num_kv_heads, page_size, head_dim], device, 16-byte aligned. LOCAL:
+ *             keys rotated at their positions; GLOBAL: the single K=V row, un-rotated (it
+ *             is rotated for the scores as it is read).
+ *   v_pages   the same shape for LOCAL; NULL for GLOBAL.
+ *   k_scales, v_scales  [num_pages, num_kv_heads, page_size] float32, device, 16-byte aligned,
+ *             for GEMMA_ATTN_PAGES_E4M3 (v_scales NULL for GLOBAL); NULL for BF16. The value
+ *             held is code * scale. gemma_attn_paged_append writes scales that are powers of
+ *             two: the smallest 2^k, k >= -126, with the row's largest magnitude <= 448 * 2^k
+ *             (1 for a row of zeros), so code * scale is a bf16 number (for scales of 2^-124
+ *             and below, rounded to one) and only the rounding to e4m3 loses anything (at the
+ *             scale 2^120, the top of bf16's range, codes stop at 240 so that none reads back as
+ *             an infinity). A row
+ *             that holds an infinity or a NaN is stored with a NaN scale and reads back as NaN.
+ *             The attention relies on power-of-two scales and on finite codes (never 0x7F / 0xFF).
+ *   block_table [batch, max_blocks] int32, device. Entries that no call's positions reach are
+ *             never read, among them, for LOCAL, those of pages wholly before the oldest
+ *             query's window: such pages may be reused. An entry that is read and lies outside
+ *             [0, num_pages) records GEMMA_ATTN_ERR_PAGE; its keys are left out (attend), its
+ *             rows not written (append), or zero (gather).
+ *   page_size 16, 32, 64, 128 or 256; num_pages * num_kv_heads < 2^31.
+ * Page rows that hold no token yet, or a token outside every query's window, may hold anything,
+ * NaN included. Among the rows that a call's queries do see, values must be finite: a row that
+ * one query of a call sees and another does not contributes 0 * value to the second.
+ * The head dims are 64, 128, 256 and 512; kinds LOCAL and GLOBAL; at most 128 query heads per
+ * KV head; batch <= 65535.
+ */
+typedef struct gemma_attn_paged_cache {
+  void* k_pages;
+  void* v_pages;
+  float* k_scales;
+  float* v_scales;
+  const int32_t* block_table;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t max_blocks;
+  int32_t dtype;
+} gemma_attn_paged_cache;
+
+/*
+ * Append to a paged cache: token i of sequence b (row cu_q[b] + i of new_k / new_v) goes to
+ * position cache_seqlens[b] + i. LOCAL keys are rotated at that position (fp32 arithmetic from
+ * the bf16 input, one rounding to the cache's type); values and GLOBAL K=V rows are stored as
+ * given, or quantised (GEMMA_ATTN_PAGES_E4M3, round to nearest even).
+ *   new_k, new_v  [total_q, num_kv_heads, head_dim] bf16, device, 16-byte aligned (new_v NULL
+ *             for GLOBAL).
+ *   cu_q      [batch + 1] int32, device, from 0, not decreasing, cu_q[batch] <= total_q. Rows
+ *             from cu_q[batch] on (a padded batch) are not stored. A sequence may have none.
+ *   cache_seqlens [batch] int32, device: tokens before the new ones (not modified).
+ * A position that is negative or at least max_blocks * page_size is not written and records
+ * GEMMA_ATTN_ERR_SEQLEN. Two sequences of one call must not write the same page row.
+ */
+int gemma_attn_paged_append(const gemma_attn_params* params, const gemma_attn_paged_cache* cache,
+                            const void* new_k, const void* new_v, const int32_t* cu_q,
+                            const int32_t* cache_seqlens, int32_t batch, int32_t total_q, void* stream);
+
+/*
+ * Read rows back: row cu_out[b] + i of out_k (and out_v) receives position starts[b] + i of
+ * sequence b as the cache holds it (LOCAL keys rotated), in bf16 (round to nearest even; exact
+ * for what gemma_attn_paged_append wrote, but for the smallest scales named above) or f32
+ * (params->out_dtype).
+ *   out_k, out_v  [total_out, num_kv_heads, head_dim], device, 16-byte aligned (out_v NULL for
+ *             GLOBAL).
+ *   starts [batch], cu_out [batch + 1] int32, device; rows from cu_out[batch] on are left as
+ *             they were. A position outside [0, max_blocks * page_size) gives a row of zeros and
+ *             records GEMMA_ATTN_ERR_SEQLEN.
+ */
+int gemma_attn_paged_gather(const gemma_attn_params* params, const gemma_attn_paged_cache* cache,
+                            const int32_t* starts, const int32_t* cu_out, void* out_k, void* out_v,
+                            int32_t batch, int32_t total_out, void* stream);
+
+/* Bytes of device workspace gemma_attn_paged_attend needs for these arguments. */
+int gemma_attn_paged_workspace_size(const gemma_attn_params* params, const gemma_attn_paged_cache* cache,
+                                    int32_t batch, int32_t total_q, int32_t max_q, int32_t max_cache_len,
+                                    size_t* bytes);
+
+/*
+ * Attention of a chunk of new tokens over a paged cache that already holds their rows (call
+ * gemma_attn_paged_append first). Query i of sequence b sits at position cache_seqlens[b] + i
+ * and sees the positions up to its own (LOCAL: the last `window` of them).
+ *   q         [total_q, num_q_heads, head_dim] bf16, device, un-rotated, 16-byte aligned.
+ *   cu_q      [batch + 1] int32, device, as in gemma_attn_paged_append: 1 new token per sequence
+ *             (decode), a few (verify), thousands (a prompt's chunk), or any mixture, 0 included.
+ *   cache_seqlens [batch] int32, device: tokens before the new ones.
+ *   out       [total_q, num_q_heads, head_dim] bf16 or f32 (params->out_dtype), device,
+ *             16-byte aligned. Rows from cu_q[batch] on are left as they were.
+ *   lse       [total_q, num_q_heads] float32 natural-log sum-exp of the scaled scores; may be NULL.
+ *   max_q, max_cache_len  upper bounds of a sequence's new tokens and of cache_seqlens. A
+ *             sequence beyond either, or past max_blocks * page_size, records
+ *             GEMMA_ATTN_ERR_SEQLEN and its rows are not written.
+ *   workspace device buffer of gemma_attn_paged_workspace_size() bytes, 256-byte aligned;
+ *             contents are scratch, nothing in it needs clearing. Calls that may run at the
+ *             same time (other streams, graphs replayed together) need one each.
+ * Keys, probabilities and rotated rows enter the products in 16 bits; scores, softmax
+ * statistics and outputs are accumulated in fp32. Over E4M3 pages the result is the attention
+ * over the values that gemma_attn_paged_gather reads back.
+ */
+int gemma_attn_paged_attend(const gemma_attn_params* params, const gemma_attn_paged_cache* cache,
+                            const void* q, const int32_t* cu_q, const int32_t* cache_seqlens, void* out,
+                            float* lse, int32_t batch, int32_t total_q, int32_t max_q,
+                            int32_t max_cache_len, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities (speculative decoding).
+ * Drafted token i of sequence b, x = draft_tokens[b][i], is accepted iff every earlier one is
+ * and uniforms[b][i] * q(x) < p(x), p = target_probs[b][i], q = draft_probs[b][i], in fp32. At
+ * the first rejection i the next token is drawn from max(p - q, 0); with all n = draft_lens[b]
+ * accepted, from target_probs[b][n]. The draw is an exponential race on the given noise: the v
+ * with the largest w(v) / noise[b][v] among those with w(v) > 0, the lowest index of a tie. A
+ * residual with no positive entry (rounding) falls back to w = p; with none there either the
+ * token is -1. Every operation is one correctly rounded fp32 operation and the maximum has no
+ * order, so the result is the same on every run.
+ *   target_probs [batch, max_draft + 1, vocab], draft_probs [batch, max_draft, vocab]:
+ *             prob_dtype (F32 or BF16), device. draft_probs NULL: the drafts were certain
+ *             (q(x) = 1), and the residual is p without x.
+ *   draft_tokens [batch, max_draft] int32; draft_lens [batch] int32 or NULL (all max_draft);
+ *             uniforms [batch, max_draft] f32 in [0, 1); noise [batch, vocab] f32, draws of
+ *             the unit exponential. Entries of noise that are not positive never win.
+ *   num_accepted [batch] int32, written; out_tokens [batch, max_draft + 1] int32, written: the
+ *             accepted tokens, the drawn one, then -1.
+ * A drafted token outside [0, vocab) is never accepted. A draft_lens entry outside
+ * [0, max_draft] is brought into that range and records GEMMA_ATTN_ERR_SEQLEN.
+ */
+int gemma_attn_draft_verify(const void* target_probs, const void* draft_probs, int32_t prob_dtype,
+                            const int32_t* draft_tokens, const int32_t* draft_lens, const float* uniforms,
+                            const float* noise, int32_t batch, int32_t max_draft, int32_t vocab,
+                            int32_t* num_accepted, int32_t* out_tokens, void* stream);
+
+/*
  * Host-side tile plan (the same rule the prefill kernels apply): for every sequence,
  * query tile of bm rows and key tile of bn keys with at least one visible pair, one
  * 4-tuple (sequence, q_tile, kv_tile, class) with class 1 = partially masked,
@@ -310,7 +452,8 @@ int gemma_attn_tile_plan(int32_t kind, int32_t window, const int32_t* cu_seqlens
                          int64_t* count);
 
 /* Synchronise `stream`, return (and clear) the device status word: GEMMA_ATTN_OK,
- * GEMMA_ATTN_ERR_TIMEOUT or GEMMA_ATTN_ERR_SEQLEN; GEMMA_ATTN_ERR_DEVICE on a CUDA error. */
+ * GEMMA_ATTN_ERR_TIMEOUT, GEMMA_ATTN_ERR_SEQLEN or GEMMA_ATTN_ERR_PAGE; GEMMA_ATTN_ERR_DEVICE on a
+ * CUDA error. */
 int gemma_attn_check(void* stream);
 
 /* Static description of a status code. */
