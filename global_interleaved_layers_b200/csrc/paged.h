@@ -89,10 +89,41 @@ struct PagedAttendArgs {
   float* partial_lse;       // [splits, T * Hq]
   int splits;               // most splits of a sequence's keys
   int row_groups;           // groups of 8 rows (query, head of the KV head's group) of the longest chunk
+  const int* chunk_of;      // [batch], >= 0: the sequence is chunk_kernel's; null: there are none
 };
 // Split-KV attention of 8 rows per warp-set over pages (paged_decode.cu), and its merge.
 cudaError_t launch_paged_rows(const PagedAttendArgs& a, bool e4m3, cudaStream_t stream);
 int paged_rows_splits(int batch, int hkv, int row_groups, int max_keys);
+
+// Long chunks (paged_chunk.cu): the device-side plan and the buffers it names, all in the
+// call's workspace.
+struct ChunkPlan {
+  int* header;              // [2]: entries of list, entries of merges
+  int* chunk_of;            // [batch]: index among the chunk sequences, or -1
+  int* tile0;               // [batch + 1]: first 128-position tile of the side copies
+  int* unit0;               // [batch + 1]: first unit
+  int4* list;               // pairs {sequence, unit of it, first key tile, end}, {partial slot or -1, -, -, -}
+  int4* merges;             // {sequence, unit of it, first slot, pieces}
+  uint16_t* q_side;         // [T, Hq, q_cols] rotated 64-dim chunks of the queries
+  uint16_t* k_rot;          // [Hkv, rot_rows, k_cols] rotated chunks of K=V keys, every tile
+  uint16_t* k_copy;         // [Hkv, copy_rows, d] bf16 rows of every tile (e4m3) or of the cut ones (bf16)
+  uint16_t* v_copy;
+  float* part_o;            // [slots, Hkv, rows, d]
+  float* part_lse;          // [slots, Hkv, rows]
+  uint32_t q_mask, k_mask;  // 64-dim chunks that come from q_side / k_rot
+  int q_cols, k_cols;
+  long long rot_rows, copy_rows;
+  int e4m3;
+  int min_rows;             // sequences with more rows per KV head than this are chunks
+  int tokens, rows;         // of a unit: tokens, and rows with their padding (128 or 256)
+  int units_x;              // units of a list entry: KV heads x output parts
+  int clusters;             // CTAs or pairs that walk the list
+};
+struct ChunkMaps {
+  CUtensorMap q, qs, k, k_rot, k_copy, v, v_copy;
+};
+cudaError_t launch_chunk(const ChunkMaps& maps, const PagedAttendArgs& a, const ChunkPlan& p, int units_bound,
+                         cudaStream_t stream);
 
 struct DraftArgs {
   const void* target;

@@ -46,27 +46,141 @@ int launched(cudaError_t e, int launches) {
   return GEMMA_ATTN_OK;
 }
 
-// Shape of an attend call: how the rows and keys are cut, and the workspace that takes.
+// Rows per KV head up to which a sequence takes the row-group kernel.
+constexpr int kChunkMinRows = 64;
+
+// How an attend call's work is cut, and what of the workspace each part takes (byte offsets).
 struct AttendPlan {
-  int row_groups, splits;
-  size_t lse_off, total;
+  int row_groups, splits;           // row-group kernel
+  size_t part_o, part_lse;
+  bool chunk;                       // some sequence may have more rows than kChunkMinRows
+  bool pair;
+  int tokens, units_x, clusters, slots, units, seqs;
+  uint32_t q_mask, k_mask;
+  long long tiles, copy_rows;
+  size_t header, chunk_of, tile0, unit0, list, merges, q_side, k_rot, k_copy, v_copy, c_part_o, c_part_lse;
+  size_t total;
 };
 
-int attend_plan(const gemma_attn_params* p, int batch, int total_q, int max_q, int max_cache_len, AttendPlan* plan) {
+int attend_plan(const gemma_attn_params* p, bool e4m3, int batch, int total_q, int max_q, int max_cache_len, AttendPlan* L) {
   if (batch < 1 || total_q < 0 || max_q < 0 || max_cache_len < 0) return GEMMA_ATTN_ERR_INVALID_ARG;
   if (batch > 65535 || (long long)max_cache_len + max_q > 0x7fffff00ll) return GEMMA_ATTN_ERR_UNSUPPORTED;
   const long long rows = (long long)total_q * p->num_q_heads;
   if (rows > 0x7fffffffll) return GEMMA_ATTN_ERR_UNSUPPORTED;
-  const int group = p->num_q_heads / p->num_kv_heads;
-  plan->row_groups = (int)(((long long)max_q * group + 7) / 8);
-  const long long keys = p->kind == GEMMA_ATTN_LOCAL ? std::min<long long>(max_cache_len, p->window) + max_q
-                                                     : (long long)max_cache_len + max_q;
-  plan->splits = paged_rows_splits(batch, p->num_kv_heads, std::max(1, plan->row_groups), (int)keys);
-  const size_t o = plan->splits > 1 ? round_up((size_t)plan->splits * rows * p->head_dim * 4, 256) : 0;
-  const size_t l = plan->splits > 1 ? round_up((size_t)plan->splits * rows * 4, 256) : 0;
-  plan->lse_off = o;
-  plan->total = o + l;
+  const int d = p->head_dim, hkv = p->num_kv_heads, group = p->num_q_heads / hkv;
+  const bool local = p->kind == GEMMA_ATTN_LOCAL;
+  *L = AttendPlan{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += round_up(bytes, 256);
+    return o;
+  };
+  const long long keys = local ? std::min<long long>(max_cache_len, p->window) + max_q : (long long)max_cache_len + max_q;
+  L->chunk = (long long)max_q * group > kChunkMinRows;
+  L->row_groups = L->chunk ? kChunkMinRows / 8 : (max_q * group + 7) / 8;
+  L->splits = paged_rows_splits(batch, hkv, std::max(1, L->row_groups), (int)keys);
+  if (L->splits > 1) {
+    L->part_o = take((size_t)L->splits * rows * d * 4);
+    L->part_lse = take((size_t)L->splits * rows * 4);
+  }
+  if (L->chunk) {
+    const int r = rotated_pairs(p->rope_p, d);
+    L->q_mask = rotated_chunk_mask(d, r);
+    L->k_mask = local ? 0u : L->q_mask;
+    L->pair = d >= 128 && (long long)max_q * group > 128;
+    L->tokens = 128 / group * (L->pair ? 2 : 1);
+    L->units_x = hkv * (d > 256 ? d / 256 : 1);
+    L->clusters = L->pair ? 74 : 148;
+    // pieces of cut units: under 4 clusters / units_x (chunk_plan_kernel)
+    L->slots = 4 * L->clusters / L->units_x + 1;
+    // chunk sequences have at least kChunkMinRows / group + 1 tokens each
+    L->seqs = std::min(batch, total_q / (kChunkMinRows / group + 1));
+    L->units = total_q / L->tokens + L->seqs;
+    const long long most = (long long)L->seqs * (((long long)max_cache_len + max_q + 127) / 128);
+    L->tiles = most;
+    if (local)  // window and chunk, and a tile that either end cuts
+      L->tiles = std::min(most, ((long long)L->seqs * p->window + total_q) / 128 + 2ll * L->seqs + 1);
+    L->copy_rows = e4m3 ? L->tiles * 128 : (long long)L->seqs * 256;
+    if (L->tiles * 128 > 0x7fffffffll) return GEMMA_ATTN_ERR_UNSUPPORTED;
+    L->header = take(8);
+    L->chunk_of = take((size_t)batch * 4);
+    L->tile0 = take(((size_t)batch + 1) * 4);
+    L->unit0 = take(((size_t)batch + 1) * 4);
+    L->list = take((size_t)(L->units + L->slots) * 32);
+    L->merges = take((size_t)L->slots * 16);
+    L->q_side = take((size_t)rows * __builtin_popcount(L->q_mask) * 128);
+    L->k_rot = take((size_t)L->tiles * 128 * hkv * __builtin_popcount(L->k_mask) * 128);
+    L->k_copy = take((size_t)L->copy_rows * hkv * d * 2);
+    L->v_copy = local ? take((size_t)L->copy_rows * hkv * d * 2) : L->k_copy;
+    const size_t prow = (size_t)L->slots * hkv * (L->pair ? 256 : 128);
+    L->c_part_o = take(prow * d * 4);
+    L->c_part_lse = take(prow * 4);
+  }
+  L->total = at;
   return GEMMA_ATTN_OK;
+}
+
+// 3-D bf16 map over [n2][n1][n0] with a {64, b1, b2} box, 128-byte swizzle.
+bool box_map(CUtensorMap* m, const void* base, long long n0, long long n1, long long n2, int b1, int b2) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)n0, (cuuint64_t)n1, (cuuint64_t)n2};
+  cuuint64_t strides[2] = {(cuuint64_t)n0 * 2, (cuuint64_t)(n0 * n1) * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)b1, (cuuint32_t)b2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int launch_attend_chunks(const gemma_attn_params* params, const PagedAttendArgs& a, bool e4m3, const AttendPlan& L,
+                         uint8_t* ws, cudaStream_t stream) {
+  ChunkPlan p{};
+  p.header = reinterpret_cast<int*>(ws + L.header);
+  p.chunk_of = reinterpret_cast<int*>(ws + L.chunk_of);
+  p.tile0 = reinterpret_cast<int*>(ws + L.tile0);
+  p.unit0 = reinterpret_cast<int*>(ws + L.unit0);
+  p.list = reinterpret_cast<int4*>(ws + L.list);
+  p.merges = reinterpret_cast<int4*>(ws + L.merges);
+  p.q_side = reinterpret_cast<uint16_t*>(ws + L.q_side);
+  p.k_rot = reinterpret_cast<uint16_t*>(ws + L.k_rot);
+  p.k_copy = reinterpret_cast<uint16_t*>(ws + L.k_copy);
+  p.v_copy = reinterpret_cast<uint16_t*>(ws + L.v_copy);
+  p.part_o = reinterpret_cast<float*>(ws + L.c_part_o);
+  p.part_lse = reinterpret_cast<float*>(ws + L.c_part_lse);
+  p.q_mask = L.q_mask;
+  p.k_mask = L.k_mask;
+  p.q_cols = __builtin_popcount(L.q_mask) * 64;
+  p.k_cols = __builtin_popcount(L.k_mask) * 64;
+  p.rot_rows = L.tiles * 128;
+  p.copy_rows = L.copy_rows;
+  p.e4m3 = e4m3 ? 1 : 0;
+  p.min_rows = kChunkMinRows;
+  p.tokens = L.tokens;
+  p.rows = L.pair ? 256 : 128;
+  p.units_x = L.units_x;
+  p.clusters = L.clusters;
+  const int d = a.c.d, hkv = a.c.hkv, ps = 1 << a.c.page_shift, tpc = 128 / a.group, keys = L.pair ? 64 : 128;
+  const long long planes = (long long)a.c.num_pages * hkv;
+  const bool local = a.c.v != nullptr;
+  ChunkMaps m;
+  bool ok = box_map(&m.q, a.q, d, a.hq, a.total_q, a.group, tpc);
+  m.qs = m.q;
+  if (L.q_mask) ok &= box_map(&m.qs, p.q_side, p.q_cols, a.hq, a.total_q, a.group, tpc);
+  ok &= box_map(&m.k_copy, p.k_copy, d, p.copy_rows, hkv, keys, 1);
+  ok &= box_map(&m.v_copy, p.v_copy, d, p.copy_rows, hkv, 128, 1);
+  m.k = m.k_copy;
+  m.v = m.v_copy;
+  if (!e4m3) {
+    ok &= box_map(&m.k, a.c.k, d, ps, planes, std::min(ps, keys), 1);
+    ok &= box_map(&m.v, local ? a.c.v : a.c.k, d, ps, planes, std::min(ps, 128), 1);
+  }
+  m.k_rot = m.k_copy;
+  if (L.k_mask) ok &= box_map(&m.k_rot, p.k_rot, p.k_cols, p.rot_rows, hkv, keys, 1);
+  if (!ok) return GEMMA_ATTN_ERR_LAUNCH;
+  const long long units = (long long)(L.units + L.slots) * L.units_x;
+  return launch_chunk(m, a, p, (int)std::min<long long>(units, 1 << 20), stream) == cudaSuccess ? GEMMA_ATTN_OK : GEMMA_ATTN_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -135,7 +249,7 @@ int gemma_attn_paged_workspace_size(const gemma_attn_params* params, const gemma
   if (rc != GEMMA_ATTN_OK) return rc;
   if (!bytes) return GEMMA_ATTN_ERR_INVALID_ARG;
   AttendPlan plan;
-  rc = attend_plan(params, batch, total_q, max_q, max_cache_len, &plan);
+  rc = attend_plan(params, e4m3, batch, total_q, max_q, max_cache_len, &plan);
   if (rc != GEMMA_ATTN_OK) return rc;
   *bytes = plan.total;
   return GEMMA_ATTN_OK;
@@ -151,7 +265,7 @@ int gemma_attn_paged_attend(const gemma_attn_params* params, const gemma_attn_pa
   int rc = paged_prepare(params, cache, &a.c, &e4m3);
   if (rc != GEMMA_ATTN_OK) return rc;
   AttendPlan plan;
-  rc = attend_plan(params, batch, total_q, max_q, max_cache_len, &plan);
+  rc = attend_plan(params, e4m3, batch, total_q, max_q, max_cache_len, &plan);
   if (rc != GEMMA_ATTN_OK) return rc;
   if (!cu_q || !cache_seqlens) return GEMMA_ATTN_ERR_INVALID_ARG;
   if (total_q == 0 || max_q == 0) return GEMMA_ATTN_OK;
@@ -178,9 +292,20 @@ int gemma_attn_paged_attend(const gemma_attn_params* params, const gemma_attn_pa
   a.softmax_scale = params->softmax_scale;
   a.row_groups = plan.row_groups;
   a.splits = plan.splits;
-  a.partial_o = static_cast<float*>(workspace);
-  a.partial_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.lse_off);
-  return launched(launch_paged_rows(a, e4m3, static_cast<cudaStream_t>(stream)), plan.splits > 1 ? 2 : 1);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.partial_o = reinterpret_cast<float*>(ws + plan.part_o);
+  a.partial_lse = reinterpret_cast<float*>(ws + plan.part_lse);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int launches = plan.splits > 1 ? 2 : 1;
+  if (plan.chunk) {
+    if (plan.seqs > 0) {
+      a.chunk_of = reinterpret_cast<int*>(ws + plan.chunk_of);
+      rc = launch_attend_chunks(params, a, e4m3, plan, ws, s);
+      if (rc != GEMMA_ATTN_OK) return rc;
+      launches += 4;
+    }
+  }
+  return launched(launch_paged_rows(a, e4m3, s), launches);
 }
 
 int gemma_attn_draft_verify(const void* target_probs, const void* draft_probs, int32_t prob_dtype,

@@ -1,0 +1,998 @@
+// paged_chunk.cu -- attention of long chunks of new tokens over a paged KV cache, on sm_100a's
+// tensor cores (tcgen05 with TMEM accumulators, TMA loads).
+//
+// The rows of a KV head are (new token, query head of its group), token-major: a 128-row tile
+// holds floor(128 / group) tokens with all the heads that share the KV head, so a short chunk
+// of a large group still fills tiles, and every row of a tile reads the same keys. A work unit
+// is one tile (two tiles in the paired form) of one KV head against a run of 128-key tiles.
+// Four launches:
+//   chunk_plan_kernel   from the lengths on the device: which sequences are chunks, their tiles,
+//                       units cut over long key ranges so that no unit is longer than half a
+//                       cluster's share, in order of size (longest first);
+//   chunk_side_kernel   what the tensor cores cannot take as it lies: rotated queries, the rotated
+//                       64-dim chunks of K=V keys ("Visual guide to Gemma 4", section "p-RoPE"),
+//                       e4m3 rows widened to bf16 (exact), and copies of the tiles that the ends
+//                       of a sequence's keys cut, with zeros beyond the ends;
+//   chunk_kernel        the attention: everything else is loaded by TMA straight from the pages,
+//                       one box per page and 64-dim chunk;
+//   chunk_merge_kernel  joins the units that were cut (log-sum-exp weights, fixed order).
+// The side copies cost bytes once per chunk while the products cost 4 d per row and key: at 256
+// rows per KV head and more the copy is a few percent of the call.
+//
+// chunk_kernel. Warp 0 loads (Q once per unit, then K and V stages through a ring), warp 1 issues
+// the MMAs (S = Q K^T into one of two TMEM buffers, O += P V with P in TMEM), warps 2-9 run the
+// softmax, two per TMEM lane quadrant, a row per lane and half the columns each, and the
+// epilogue. The order S(j), PV(j-1), S(j+1) ... keeps the tensor core on the next scores while
+// P(j) is formed. Persistent CTAs (pairs) walk the unit list in snake order. Paired form
+// (cta_group::2, head dims >= 128, more than 128 rows): each CTA of a pair owns 128 of 256 rows
+// and loads half of every K and V stage, halving the bytes per product. At head dim 512 a unit
+// accumulates 256 of the output columns (a 128 x 512 fp32 tile would fill TMEM) and the scores
+// are computed by both halves.
+// Bound: the tensor pipe for long chunks (scores once more at d = 512); launch and copy latency
+// for short ones.
+#include "paged.h"
+#include "tile_plan.h"
+
+namespace gattn {
+
+namespace {
+
+constexpr int kCM = 128;                     // rows per CTA
+constexpr int kCN = 128;                     // keys per tile
+constexpr int kCThreads = 320;
+constexpr int kCChunkBytes = 16384;          // 128 rows x 64 dims
+constexpr int kCMaxStages = 16;
+constexpr int kCBarBytes = 2048;
+
+template <int D, bool PAIR>
+struct ChunkCfg {
+  static constexpr int kDv = D > 256 ? 256 : D;               // output columns per unit
+  static constexpr int kParts = D / kDv;
+  static constexpr int kQChunks = D / 64;
+  static constexpr int kVChunks = kDv / 64;
+  static constexpr int kQBytes = kQChunks * kCChunkBytes;
+  // Single: a stage is one 64-dim chunk of 128 keys (K) or one 64-column chunk (V). Pair at
+  // d >= 256: four chunks of the CTA's 64 keys, or two column chunks of 128 keys; at 128: half.
+  static constexpr int kStageBytes = (PAIR && D >= 256) ? 2 * kCChunkBytes : kCChunkBytes;
+  static constexpr int kKeys = PAIR ? 64 : 128;               // keys of a K stage in this CTA
+  static constexpr int kKChunkBytes = kKeys * 128;
+  static constexpr int kKPerStage = kStageBytes / kKChunkBytes;
+  static constexpr int kVPerStage = kStageBytes / kCChunkBytes;
+  static constexpr int kKStages = kQChunks / kKPerStage;
+  static constexpr int kVStages = (PAIR ? kVChunks / 2 : kVChunks) / kVPerStage;
+  static constexpr int kPvN = (PAIR ? 2 : 1) * kVPerStage * 64;
+  static constexpr int kRing = 232448 - 1024 - kCBarBytes - kQBytes;
+  static constexpr int kStages = kRing / kStageBytes < kCMaxStages ? kRing / kStageBytes : kCMaxStages;
+  static constexpr int kSmemData = kQBytes + kStages * kStageBytes;
+  static constexpr int kSmemBytes = kSmemData + 1024 + kCBarBytes;
+  static_assert(!PAIR || D >= 128, "paired form needs two 64-dim chunks");
+  static_assert(kKStages >= 1 && kVStages >= 1 && kStages >= 2 && kPvN <= 256, "ring shape");
+};
+
+struct __align__(8) ChunkBars {
+  uint64_t q_full, q_empty, o_ready, o_empty, mma_done;
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t ring_full[kCMaxStages], ring_empty[kCMaxStages];
+  uint64_t xfull[4], xfree[4];
+  uint32_t tmem_base;
+  int abort_flag;
+  float xch[2 * 128];
+};
+static_assert(sizeof(ChunkBars) <= kCBarBytes, "barrier block");
+
+// Tiles [lo, hi) of 128 positions that the tokens [t0, t1] of a sequence see, `len` tokens
+// before the chunk.
+__device__ __forceinline__ void chunk_tiles(const PagedAttendArgs& a, int len, int t0, int t1, int* lo, int* hi) {
+  *lo = keys_first(a, len, t0) / kCN;
+  *hi = (len + t1) / kCN + 1;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Plan: one block. All sums are over lengths only, so every call with the same lengths cuts the
+// work alike; the order within a size class (and which partial slot a cut unit gets) may vary
+// and enters no result.
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanBuckets = 1024;
+
+// Inclusive scan of v over the block; *total gets the sum.
+__device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, v, m);
+    if (lane >= m) v += o;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int w = s_warp[lane];
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, w, m);
+      if (lane >= m) w += o;
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  *total = s_warp[31];
+  return v + (warp ? s_warp[warp - 1] : 0);
+}
+}  // namespace
+
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PagedAttendArgs a, ChunkPlan p) {
+  __shared__ int s_warp[32];
+  __shared__ int s_hist[kPlanBuckets];
+  __shared__ int s_slots, s_merges;
+  __shared__ unsigned long long s_work;
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    s_slots = s_merges = 0;
+    s_work = 0;
+  }
+  for (int i = tid; i < kPlanBuckets; i += kPlanThreads) s_hist[i] = 0;
+  // The workspace is sized for lengths that add up to at most total_q, which seq_ok and
+  // prefixes that do not decrease ensure; with one that does, there are no chunks.
+  int down = 0;
+  for (int b = tid; b < a.batch; b += kPlanThreads) down |= __ldg(a.cu_q + b + 1) < __ldg(a.cu_q + b);
+  down = __syncthreads_or(down);
+  // ---- sequences: chunk index, first side tile, first unit
+  int chunks = 0, tiles = 0, units = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int is = 0, nt = 0, nu = 0;
+    if (b < a.batch) {
+      const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0, len = __ldg(a.lens + b);
+      if (n != 0 && !seq_ok(a, tok0, n, len)) {
+        atomicOr(&g_status, kStatusSeqlen);
+      } else if (!down && n > 0 && (long long)n * a.group > p.min_rows) {
+        int lo, hi;
+        chunk_tiles(a, len, 0, n - 1, &lo, &hi);
+        is = 1;
+        nt = hi - lo;
+        nu = (n + p.tokens - 1) / p.tokens;
+      }
+    }
+    int ti, tt, tu;
+    const int ci = block_scan(is, s_warp, &ti), ct = block_scan(nt, s_warp, &tt), cu = block_scan(nu, s_warp, &tu);
+    if (b < a.batch) {
+      p.chunk_of[b] = is ? chunks + ci - 1 : -1;
+      p.tile0[b] = tiles + ct - nt;
+      p.unit0[b] = units + cu - nu;
+    }
+    chunks += ti;
+    tiles += tt;
+    units += tu;
+  }
+  if (tid == 0) {
+    p.tile0[a.batch] = tiles;
+    p.unit0[a.batch] = units;
+  }
+  __syncthreads();
+  // ---- work: key tiles of every unit
+  auto unit = [&](int u, int* b, int* qt, int* lo, int* hi) {
+    int x = 0, y = a.batch;  // the last sequence with unit0 <= u (sequences without units share a value)
+    while (y - x > 1) {
+      const int m = (x + y) >> 1;
+      if (p.unit0[m] <= u) x = m;
+      else y = m;
+    }
+    *b = x;
+    *qt = u - p.unit0[x];
+    const int n = __ldg(a.cu_q + x + 1) - __ldg(a.cu_q + x), t0 = *qt * p.tokens;
+    chunk_tiles(a, __ldg(a.lens + x), t0, min(t0 + p.tokens, n) - 1, lo, hi);
+  };
+  unsigned long long mine = 0;
+  for (int u = tid; u < units; u += kPlanThreads) {
+    int b, qt, lo, hi;
+    unit(u, &b, &qt, &lo, &hi);
+    mine += hi - lo;
+  }
+  if (mine) atomicAdd(&s_work, mine);
+  __syncthreads();
+  // Most tiles of a piece: half a cluster's share of the work, at least four (a cut costs a
+  // fp32 tile written and read again). With w = s_work the pieces of units that are cut
+  // number under 2 w / most <= 4 clusters / units_x.
+  const long long share = ((long long)s_work * p.units_x + 2 * p.clusters - 1) / (2 * p.clusters);
+  const int most = (int)max(share, (long long)4);
+  auto pieces = [&](int nt) { return nt > most ? (nt + most - 1) / most : 1; };
+  for (int u = tid; u < units; u += kPlanThreads) {
+    int b, qt, lo, hi;
+    unit(u, &b, &qt, &lo, &hi);
+    const int nt = hi - lo, ns = pieces(nt), per = (nt + ns - 1) / ns;
+    atomicAdd(&s_hist[kPlanBuckets - 1 - min(per, kPlanBuckets - 1)], ns);
+  }
+  __syncthreads();
+  int total;
+  {
+    const int v = s_hist[tid], incl = block_scan(v, s_warp, &total);
+    s_hist[tid] = incl - v;
+  }
+  __syncthreads();
+  for (int u = tid; u < units; u += kPlanThreads) {
+    int b, qt, lo, hi;
+    unit(u, &b, &qt, &lo, &hi);
+    const int nt = hi - lo, ns = pieces(nt), per = (nt + ns - 1) / ns;
+    int slot = 0;
+    if (ns > 1) {
+      slot = atomicAdd(&s_slots, ns);
+      p.merges[atomicAdd(&s_merges, 1)] = make_int4(b, qt, slot, ns);
+    }
+    const int at = atomicAdd(&s_hist[kPlanBuckets - 1 - min(per, kPlanBuckets - 1)], ns);
+    for (int s = 0; s < ns; ++s) {
+      // ns pieces of at most `per` tiles; rounding may leave a late one empty: it is then skipped
+      const int k0 = min(lo + s * per, hi), k1 = min(k0 + per, hi);
+      p.list[2 * (at + s)] = make_int4(b, qt, k0, k1);
+      p.list[2 * (at + s) + 1] = make_int4(ns > 1 ? slot + s : -1, 0, 0, 0);
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    p.header[0] = total;
+    p.header[1] = s_merges;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Side copies.
+// ---------------------------------------------------------------------------
+namespace {
+
+// Column of a side copy that holds `dim`, or -1 when its 64-dim chunk is not copied.
+__device__ __forceinline__ int chunk_col(uint32_t mask, int dim) {
+  const int c = dim >> 6;
+  if (!((mask >> c) & 1u)) return -1;
+  return __popc(mask & ((1u << c) - 1u)) * 64 + (dim & 63);
+}
+
+__device__ __forceinline__ void turn8(const float* x0, const float* x1, const float* c, const float* s, float* y0, float* y1) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    y0[e] = x0[e] * c[e] - x1[e] * s[e];
+    y1[e] = x0[e] * s[e] + x1[e] * c[e];
+  }
+}
+
+// 8 elements of a page row, in fp32.
+template <bool E4M3>
+__device__ __forceinline__ void load8(const uint8_t* row, int dim, float scale, float* f) {
+  if constexpr (E4M3) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(row + dim));
+    e4m3x4_to_f32(w.x, f);
+    e4m3x4_to_f32(w.y, f + 4);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= scale;
+  } else {
+    bf8_to_f32(__ldg(reinterpret_cast<const uint4*>(row + 2 * dim)), f);
+  }
+}
+
+constexpr int kSideThreads = 256;
+constexpr int kSideRows = 32;  // rows of a block's step: 8 threads a row
+
+}  // namespace
+
+// Blocks walk first the query rows (32 tokens a step), then the key rows (a quarter of a tile a
+// step). A thread owns 8 pairs (j, j + d/2) of a row, computes their angles once and goes over
+// the heads.
+template <bool E4M3>
+__global__ void __launch_bounds__(kSideThreads) chunk_side_kernel(PagedAttendArgs a, ChunkPlan p) {
+  const int d = a.c.d, half = d / 2, groups = d / 16, hkv = a.c.hkv;
+  const int row = threadIdx.x >> 3, lane8 = threadIdx.x & 7;
+  const int qsteps = p.q_mask ? (a.total_q + kSideRows - 1) / kSideRows : 0;
+  const long long steps = qsteps + (long long)p.tile0[a.batch] * (kCN / kSideRows);
+  for (long long step = blockIdx.x; step < steps; step += gridDim.x) {
+    if (step < qsteps) {
+      const int t = (int)step * kSideRows + row;
+      if (t >= a.total_q || t >= __ldg(a.cu_q + a.batch) || t < __ldg(a.cu_q)) continue;
+      const int b = seq_of_row(a.cu_q, a.batch, t);
+      if (p.chunk_of[b] < 0) continue;
+      const double pos = (double)(__ldg(a.lens + b) + t - __ldg(a.cu_q + b));
+      for (int g = lane8; g < groups; g += 8) {
+        const int j0 = 8 * g, c0 = chunk_col(p.q_mask, j0), c1 = chunk_col(p.q_mask, j0 + half);
+        if (c0 < 0 && c1 < 0) continue;
+        float c[8], s[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          c[e] = 1.f;
+          s[e] = 0.f;
+          if (j0 + e < a.r) rope_cos_sin(pos, rope_inv_freq_turns(j0 + e, d, a.log2_base), &c[e], &s[e]);
+        }
+        for (int h = 0; h < a.hq; ++h) {
+          const uint16_t* src = a.q + ((size_t)t * a.hq + h) * d;
+          uint16_t* dst = p.q_side + ((size_t)t * a.hq + h) * p.q_cols;
+          float x0[8], x1[8], y0[8], y1[8];
+          bf8_to_f32(__ldg(reinterpret_cast<const uint4*>(src + j0)), x0);
+          bf8_to_f32(__ldg(reinterpret_cast<const uint4*>(src + j0 + half)), x1);
+          turn8(x0, x1, c, s, y0, y1);
+          if (c0 >= 0) *reinterpret_cast<uint4*>(dst + c0) = f32_to_bf8(y0);
+          if (c1 >= 0) *reinterpret_cast<uint4*>(dst + c1) = f32_to_bf8(y1);
+        }
+      }
+      continue;
+    }
+    const int tile = (int)((step - qsteps) / (kCN / kSideRows));
+    const int in_tile = (int)((step - qsteps) % (kCN / kSideRows)) * kSideRows + row;
+    int b = 0, y = a.batch;
+    while (y - b > 1) {
+      const int m = (b + y) >> 1;
+      if (p.tile0[m] <= tile) b = m;
+      else y = m;
+    }
+    const int n = __ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b), len = __ldg(a.lens + b);
+    const int first = keys_first(a, len, 0), end = len + n;
+    const int kt = first / kCN + tile - p.tile0[b];
+    const bool head_cut = kt * kCN < first, tail_cut = (kt + 1) * kCN > end;
+    const bool copy = E4M3 || head_cut || tail_cut;
+    if (!copy && !p.k_mask) continue;
+    const int pos = kt * kCN + in_tile;
+    bool have = pos >= first && pos < end;
+    size_t src = 0;
+    if (have) {
+      const int page = page_of(a.c, b, pos >> a.c.page_shift);
+      have = page >= 0;
+      src = have ? page_row(a.c, page, 0, pos & ((1 << a.c.page_shift) - 1)) : 0;
+    }
+    const size_t head_step = (size_t)1 << a.c.page_shift;
+    const size_t side_row = (size_t)tile * kCN + in_tile;
+    const size_t copy_row = E4M3 ? side_row : ((size_t)2 * p.chunk_of[b] + (tail_cut ? 1 : 0)) * kCN + in_tile;
+    const int esz = E4M3 ? 1 : 2;
+    for (int g = lane8; g < groups; g += 8) {
+      const int j0 = 8 * g, c0 = chunk_col(p.k_mask, j0), c1 = chunk_col(p.k_mask, j0 + half);
+      const bool rot = c0 >= 0 || c1 >= 0;
+      if (!rot && !copy) continue;
+      float c[8], s[8];
+      if (rot) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          c[e] = 1.f;
+          s[e] = 0.f;
+          if (j0 + e < a.r) rope_cos_sin((double)pos, rope_inv_freq_turns(j0 + e, d, a.log2_base), &c[e], &s[e]);
+        }
+      }
+      for (int h = 0; h < hkv; ++h) {
+        float x0[8] = {}, x1[8] = {}, y0[8], y1[8];
+        const size_t at = src + h * head_step;
+        if (have) {
+          const float sc = E4M3 ? __ldg(a.c.k_scales + at) : 1.f;
+          load8<E4M3>(a.c.k + at * d * esz, j0, sc, x0);
+          load8<E4M3>(a.c.k + at * d * esz, j0 + half, sc, x1);
+        }
+        if (rot) {
+          uint16_t* dst = p.k_rot + ((size_t)h * p.rot_rows + side_row) * p.k_cols;
+          turn8(x0, x1, c, s, y0, y1);
+          if (c0 >= 0) *reinterpret_cast<uint4*>(dst + c0) = f32_to_bf8(y0);
+          if (c1 >= 0) *reinterpret_cast<uint4*>(dst + c1) = f32_to_bf8(y1);
+        }
+        if (copy) {
+          uint16_t* dst = p.k_copy + ((size_t)h * p.copy_rows + copy_row) * d;
+          *reinterpret_cast<uint4*>(dst + j0) = f32_to_bf8(x0);
+          *reinterpret_cast<uint4*>(dst + j0 + half) = f32_to_bf8(x1);
+          if (a.c.v != nullptr) {
+            float v0[8] = {}, v1[8] = {};
+            if (have) {
+              const float sc = E4M3 ? __ldg(a.c.v_scales + at) : 1.f;
+              load8<E4M3>(a.c.v + at * d * esz, j0, sc, v0);
+              load8<E4M3>(a.c.v + at * d * esz, j0 + half, sc, v1);
+            }
+            dst = p.v_copy + ((size_t)h * p.copy_rows + copy_row) * d;
+            *reinterpret_cast<uint4*>(dst + j0) = f32_to_bf8(v0);
+            *reinterpret_cast<uint4*>(dst + j0 + half) = f32_to_bf8(v1);
+          }
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The attention kernel.
+// ---------------------------------------------------------------------------
+template <int D, bool PAIR>
+__global__ void __launch_bounds__(kCThreads, 1)
+chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ PagedAttendArgs a,
+             const __grid_constant__ ChunkPlan p) {
+  using Cfg = ChunkCfg<D, PAIR>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_smem = smem;
+  uint8_t* ring = smem + Cfg::kQBytes;
+  ChunkBars* bars = reinterpret_cast<ChunkBars*>(smem + Cfg::kSmemData);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const int tpc = p.tokens / (PAIR ? 2 : 1);  // tokens of one CTA's tile
+
+  // ---- the unit schedule: snake order over the list, which runs from long to short
+  const int num_units = p.header[0] * p.units_x;
+  const int nclusters = (int)gridDim.x / (PAIR ? 2 : 1);
+  const int cid = (int)blockIdx.x / (PAIR ? 2 : 1);
+  const int nrounds = (num_units + nclusters - 1) / nclusters;
+  struct Unit {
+    int b, kvh, part, tok0, n, len, t0, kt_lo, ntiles, slot;
+  };
+  auto unit_of_round = [&](int r, Unit& w) -> bool {
+    const int u = r * nclusters + ((r & 1) ? nclusters - 1 - cid : cid);
+    if (u >= num_units) return false;
+    const int ux = u % p.units_x;
+    const int4 e = __ldg(p.list + 2 * (u / p.units_x)), f = __ldg(p.list + 2 * (u / p.units_x) + 1);
+    w.b = e.x;
+    w.part = ux % Cfg::kParts;
+    w.kvh = ux / Cfg::kParts;
+    w.tok0 = __ldg(a.cu_q + e.x);
+    w.n = __ldg(a.cu_q + e.x + 1) - w.tok0;
+    w.len = __ldg(a.lens + e.x);
+    w.t0 = e.y * p.tokens;
+    w.kt_lo = e.z;
+    w.ntiles = e.w - e.z;
+    w.slot = f.x;
+    return true;  // a piece without tiles writes an empty partial
+  };
+
+  if (threadIdx.x == 0) {
+    const uint32_t loads = PAIR ? 2u : 1u;
+    mbar_init(&bars->q_full, loads);
+    mbar_init(&bars->q_empty, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->s_full[b], 1);
+      mbar_init(&bars->p_full[b], PAIR ? 16 : 8);
+      mbar_init(&bars->pv_done[b], 1);
+    }
+    mbar_init(&bars->o_ready, 1);
+    mbar_init(&bars->o_empty, PAIR ? 16 : 8);
+    mbar_init(&bars->mma_done, 1);
+    for (int q = 0; q < 4; ++q) {
+      mbar_init(&bars->xfull[q], 2);
+      mbar_init(&bars->xfree[q], 2);
+    }
+    for (int s = 0; s < Cfg::kStages; ++s) {
+      mbar_init(&bars->ring_full[s], loads);
+      mbar_init(&bars->ring_empty[s], 1);
+    }
+    bars->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(&bars->tmem_base, kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&bars->tmem_base, kTmemCols);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) {
+    __syncwarp();
+    cluster_sync_all();
+  }
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  volatile int* abort_flag = &bars->abort_flag;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (whole warp: a lane per box)
+    auto expect = [&](uint64_t* bar, uint32_t bytes) {
+      if (!PAIR || leader) mbar_arrive_expect_tx(bar, bytes);
+      else mbar_arrive_expect_tx_cluster(smem_u32(bar) & kPeerBitMask, bytes);
+    };
+    auto load = [&](void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+      if constexpr (PAIR) tma_load_3d_pair(dst, map, bar, c0, c1, c2);
+      else tma_load_3d(dst, map, bar, c0, c1, c2);
+    };
+    auto col_of = [](uint32_t mask, int c) { return __popc(mask & ((1u << c) - 1u)) * 64; };
+    const int ps = 1 << a.c.page_shift;
+    const int kbox = min(ps, Cfg::kKeys), vbox = min(ps, kCN);      // rows of a page box
+    const int kboxes = Cfg::kKeys / kbox, vboxes = kCN / vbox;
+    const int out_plane = a.c.num_pages * a.c.hkv;                  // past the pool: a box of zeros
+    int st = 0;
+    uint32_t ph = 0;
+    auto next = [&]() { if (++st == Cfg::kStages) { st = 0; ph ^= 1u; } };
+    bool ok = true;
+    int unit_iter = 0, q_issued = 0;
+    for (int r = 0; r < nrounds && ok; ++r) {
+      Unit w;
+      if (!unit_of_round(r, w)) continue;
+      if (w.ntiles == 0) continue;
+      if (unit_iter > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (uint32_t)(unit_iter - 1) & 1u, abort_flag));
+        if (!ok) break;
+      }
+      if (lane == 0) expect(&bars->q_full, Cfg::kQChunks * 128u * (uint32_t)(tpc * a.group));
+      __syncwarp();
+      if (lane < Cfg::kQChunks) {
+        const int c = lane;
+        const bool rot = (p.q_mask >> c) & 1u;
+        load(q_smem + c * kCChunkBytes, rot ? &maps.qs : &maps.q, &bars->q_full, rot ? col_of(p.q_mask, c) : c * 64,
+             w.kvh * a.group, w.tok0 + w.t0 + (int)rank * tpc);
+      }
+      ++q_issued;
+      const int first = keys_first(a, w.len, 0), end = w.len + w.n, seq_kt0 = first / kCN;
+      const int side0 = p.tile0[w.b];
+      const int edge0 = 2 * p.chunk_of[w.b];
+      // Rows of tile kt in the copies: -1 when the tile is read from the pages.
+      auto copy_row = [&](int kt) -> int {
+        if (p.e4m3) return (side0 + kt - seq_kt0) * kCN;
+        if ((kt + 1) * kCN > end) return (edge0 + 1) * kCN;
+        if (kt * kCN < first) return edge0 * kCN;
+        return -1;
+      };
+      // Plane (page, head) of position pos, for interior tiles.
+      auto plane_of = [&](int pos) -> int {
+        const int pg = page_of(a.c, w.b, pos >> a.c.page_shift);
+        return pg < 0 ? out_plane : pg * a.c.hkv + w.kvh;
+      };
+      // The table entries of a tile are read one tile ahead: this lane's box of the next K
+      // stages and of the next V stages.
+      const int kpos = (int)rank * (PAIR ? 64 : 0) + (lane % kboxes) * kbox, vpos = (lane % vboxes) * vbox;
+      auto k_plane = [&](int kt) { return copy_row(kt) < 0 ? plane_of(kt * kCN + kpos) : 0; };
+      auto v_plane = [&](int kt) { return copy_row(kt) < 0 ? plane_of(kt * kCN + vpos) : 0; };
+      int kpl = k_plane(w.kt_lo), vpl = 0, vpl_next = v_plane(w.kt_lo);
+      for (int jj = 0; jj <= w.ntiles && ok; ++jj) {
+        if (jj < w.ntiles) {
+          const int kt = w.kt_lo + jj, cr = copy_row(kt);
+          const int kpl_next = jj + 1 < w.ntiles ? k_plane(kt + 1) : 0;
+          for (int s = 0; s < Cfg::kKStages && ok; ++s) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->ring_empty[st], ph ^ 1u, abort_flag));
+            if (!ok) break;
+            uint64_t* bar = &bars->ring_full[st];
+            if (lane == 0) expect(bar, Cfg::kStageBytes);
+            __syncwarp();
+            uint8_t* dst = ring + st * Cfg::kStageBytes;
+            // lanes [0, kKPerStage * kboxes): chunk sub = lane / kboxes, box lane % kboxes
+            const int sub = lane / kboxes, box = lane % kboxes;
+            if (sub < Cfg::kKPerStage) {
+              const int c = Cfg::kKPerStage * s + sub;
+              uint8_t* d0 = dst + sub * Cfg::kKChunkBytes;
+              if ((p.k_mask >> c) & 1u) {
+                if (box == 0)
+                  load(d0, &maps.k_rot, bar, col_of(p.k_mask, c), (side0 + kt - seq_kt0) * kCN + (int)rank * (PAIR ? 64 : 0), w.kvh);
+              } else if (cr >= 0) {
+                if (box == 0) load(d0, &maps.k_copy, bar, c * 64, cr + (int)rank * (PAIR ? 64 : 0), w.kvh);
+              } else {
+                load(d0 + box * kbox * 128, &maps.k, bar, c * 64, (kt * kCN + kpos) & (ps - 1), kpl);
+              }
+            }
+            next();
+          }
+          kpl = kpl_next;
+        }
+        if (jj >= 1) {
+          const int kt = w.kt_lo + jj - 1, cr = copy_row(kt);
+          vpl = vpl_next;
+          if (jj < w.ntiles) vpl_next = v_plane(kt + 1);
+          for (int s = 0; s < Cfg::kVStages && ok; ++s) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->ring_empty[st], ph ^ 1u, abort_flag));
+            if (!ok) break;
+            uint64_t* bar = &bars->ring_full[st];
+            if (lane == 0) expect(bar, Cfg::kStageBytes);
+            __syncwarp();
+            const int sub = lane / vboxes, box = lane % vboxes;
+            if (sub < Cfg::kVPerStage) {
+              const int c = ((PAIR ? 2 * s + (int)rank : s) * Cfg::kVPerStage) + sub;
+              uint8_t* d0 = ring + st * Cfg::kStageBytes + sub * kCChunkBytes;
+              if (cr >= 0) {
+                if (box == 0) load(d0, &maps.v_copy, bar, w.part * Cfg::kDv + c * 64, cr, w.kvh);
+              } else {
+                load(d0 + box * vbox * 128, &maps.v, bar, w.part * Cfg::kDv + c * 64, (kt * kCN + vpos) & (ps - 1), vpl);
+              }
+            }
+            next();
+          }
+        }
+      }
+      ++unit_iter;
+    }
+    // Copies counted on this CTA's barriers land before it can leave: the last fill of each
+    // slot (its phase has parity ph ^ 1 in the order walked here) and the last Q. The odd CTA's
+    // copies complete on the even CTA's barriers, which waits for them before the pair leaves.
+    if (lane == 0 && (!PAIR || leader)) {
+      for (int s = 0; s < Cfg::kStages; ++s) {
+        const unsigned long long w0 = globaltimer_ns();
+        while (!mbar_try_wait(&bars->ring_full[st], ph ^ 1u) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+        next();
+      }
+      if (q_issued > 0) {
+        const unsigned long long w0 = globaltimer_ns();
+        while (!mbar_try_wait(&bars->q_full, (uint32_t)(q_issued - 1) & 1u) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (lane == 0 && leader) {
+      constexpr int M = PAIR ? 2 * kCM : kCM;
+      constexpr int PV_N = Cfg::kPvN;
+      const uint32_t idesc_qk = umma_idesc_bf16(M, kCN, 0, 0);
+      const uint32_t idesc_pv = umma_idesc_bf16(M, PV_N, 0, 1);
+      const uint64_t q_desc0 = sdesc_sw128(smem_u32(q_smem), 16, 1024);
+      const uint64_t k_desc0 = sdesc_sw128(smem_u32(ring), 16, 1024);
+      const uint64_t v_desc0 = sdesc_sw128(smem_u32(ring), kCChunkBytes, 1024);
+      auto commit_both = [&](uint64_t* bar) {
+        if constexpr (PAIR) umma_commit_pair_both(bar);
+        else umma_commit(bar);
+      };
+      int st = 0;
+      uint32_t ph = 0;
+      auto next = [&]() { if (++st == Cfg::kStages) { st = 0; ph ^= 1u; } };
+      bool ok = true;
+      int g = 0;  // tiles of earlier units
+      int unit_iter = 0;
+      for (int r = 0; r < nrounds && ok; ++r) {
+        Unit w;
+        if (!unit_of_round(r, w)) continue;
+        if (w.ntiles == 0) continue;
+        ok = wait_bar<PAIR>(&bars->q_full, (uint32_t)unit_iter & 1u, abort_flag);
+        for (int jj = 0; jj <= w.ntiles && ok; ++jj) {
+          if (jj < w.ntiles) {
+            const int t = g + jj;
+            const uint32_t s_col = (t & 1) ? kColS1 : kColS0;
+            // S(t) overwrites the buffer whose P fed PV(t - 2)
+            if (t >= 2) ok = wait_bar<PAIR>(&bars->pv_done[t & 1], (uint32_t)((t - 2) >> 1) & 1u, abort_flag);
+            tc_fence_after();
+            for (int s = 0; s < Cfg::kKStages && ok; ++s) {
+              ok = wait_bar<PAIR>(&bars->ring_full[st], ph, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t kd = k_desc0 + (uint64_t)((st * Cfg::kStageBytes) >> 4);
+#pragma unroll
+              for (int sub = 0; sub < Cfg::kKPerStage; ++sub) {
+                const int c = Cfg::kKPerStage * s + sub;
+                const uint64_t qd = q_desc0 + (uint64_t)((c * kCChunkBytes) >> 4);
+                const uint64_t kds = kd + (uint64_t)((sub * Cfg::kKChunkBytes) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  if constexpr (PAIR) umma_ss_pair(tmem + s_col, qd + 2 * kk, kds + 2 * kk, idesc_qk, (c | kk) != 0);
+                  else umma_ss(tmem + s_col, qd + 2 * kk, kds + 2 * kk, idesc_qk, (c | kk) != 0);
+                }
+              }
+              commit_both(&bars->ring_empty[st]);
+              next();
+            }
+            if (!ok) break;
+            commit_both(&bars->s_full[t & 1]);
+            if (jj == w.ntiles - 1) commit_both(&bars->q_empty);  // the unit's last read of Q
+          }
+          if (jj >= 1) {
+            const int pt = g + jj - 1;
+            const uint32_t p_col = (pt & 1) ? kColS1 : kColS0;
+            ok = wait_bar<PAIR>(&bars->p_full[pt & 1], (uint32_t)(pt >> 1) & 1u, abort_flag);
+            if (!ok) break;
+            // the unit's first value MMA overwrites O: the previous unit's epilogue has read it
+            if (jj == 1 && unit_iter > 0) {
+              ok = wait_bar<PAIR>(&bars->o_empty, (uint32_t)(unit_iter - 1) & 1u, abort_flag);
+              if (!ok) break;
+            }
+            tc_fence_after();
+            for (int s = 0; s < Cfg::kVStages && ok; ++s) {
+              ok = wait_bar<PAIR>(&bars->ring_full[st], ph, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t vd = v_desc0 + (uint64_t)((st * Cfg::kStageBytes) >> 4);
+              const uint32_t o_col = kColO + s * PV_N;
+#pragma unroll
+              for (int kk = 0; kk < kCN / 16; ++kk) {
+                const bool acc = (jj - 1) != 0 || kk != 0;
+                if constexpr (PAIR) umma_ts_pair(tmem + o_col, tmem + p_col + kk * 8, vd + 128 * kk, idesc_pv, acc);
+                else umma_ts(tmem + o_col, tmem + p_col + kk * 8, vd + 128 * kk, idesc_pv, acc);
+              }
+              commit_both(&bars->ring_empty[st]);
+              next();
+            }
+            if (!ok) break;
+            commit_both(&bars->pv_done[pt & 1]);
+          }
+        }
+        if (!ok) break;
+        commit_both(&bars->o_ready);
+        g += w.ntiles;
+        ++unit_iter;
+      }
+      if constexpr (PAIR) umma_commit_pair_local(&bars->mma_done);
+      else umma_commit(&bars->mma_done);
+      const unsigned long long w0 = globaltimer_ns();
+      while (!mbar_try_wait(&bars->mma_done, 0) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+    }
+  } else {
+    // ------------------------------------------------------------ softmax + epilogue
+    const int quad = warp & 3;
+    const int half = (warp - 2) >> 2;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const float coef = a.softmax_scale * 1.4426950408889634f;
+    constexpr int kHC = kCN / 2;
+    constexpr int kHO = Cfg::kDv / 2;
+    float* xch = bars->xch;
+    uint32_t xk = 0;
+    auto exchange = [&](float v, bool& okx) -> float {
+      xch[half * kCM + row] = v;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->xfull[quad]);
+      okx = __all_sync(0xffffffffu, mbar_wait(&bars->xfull[quad], xk & 1u, abort_flag));
+      tc_fence_after();
+      const float other = okx ? xch[(1 - half) * kCM + row] : v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->xfree[quad]);
+      if (okx) okx = __all_sync(0xffffffffu, mbar_wait(&bars->xfree[quad], xk & 1u, abort_flag));
+      ++xk;
+      return other;
+    };
+    const int row_tok = row / a.group, row_head = row - row_tok * a.group;  // this row's token and head in the tile
+    bool ok = true;
+    int g = 0, unit_iter = 0;
+    for (int r = 0; r < nrounds && ok; ++r) {
+      Unit w;
+      if (!unit_of_round(r, w)) continue;
+      const int tile_t0 = w.t0 + (int)rank * tpc;        // first token of this CTA's tile
+      const int tok = tile_t0 + row_tok;
+      const bool valid = row_tok < tpc && tok < w.n;
+      const size_t part_row = ((size_t)max(w.slot, 0) * a.c.hkv + w.kvh) * (PAIR ? 256 : 128) + rank * 128 + row;
+      if (w.ntiles == 0) {  // an empty piece of a cut unit
+        if (half == 0 && w.part == 0) p.part_lse[part_row] = -INFINITY;
+        continue;
+      }
+      const int qpos = w.len + tok;
+      // every row of this tile sees every key of a tile at or before min_q and after max_q - window
+      const int min_q = w.len + tile_t0, max_q = w.len + max(min(tile_t0 + tpc, w.n), tile_t0 + 1) - 1;
+      float m_used = -INFINITY;
+      float l_part = 0.f;
+      for (int jj = 0; jj < w.ntiles && ok; ++jj) {
+        const int t = g + jj, b = t & 1;
+        const uint32_t s_col = (b ? kColS1 : kColS0) + half * kHC;
+        ok = __all_sync(0xffffffffu, wait_bar<PAIR>(&bars->s_full[b], (uint32_t)(t >> 1) & 1u, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        float sv[kHC];
+        uint32_t* tr = reinterpret_cast<uint32_t*>(sv);
+#pragma unroll
+        for (int c = 0; c < kHC / 32; ++c) tmem_ld_x32(tmem + lane_off + s_col + c * 32, tr + c * 32);
+        tmem_ld_wait();
+        const int k_tile = (w.kt_lo + jj) * kCN;
+        const bool partial = k_tile + kCN - 1 > min_q || (a.is_local && k_tile <= max_q - a.window);
+        float mx8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx8[i] = -INFINITY;
+        if (partial) {
+          const int k0 = k_tile + half * kHC;
+          const int c_hi = qpos - k0;
+          const int c_lo = a.is_local ? qpos - a.window + 1 - k0 : 0;
+#pragma unroll
+          for (int c = 0; c < kHC; ++c) {
+            sv[c] = (c >= c_lo && c <= c_hi) ? sv[c] : -INFINITY;
+            mx8[c & 7] = fmaxf(mx8[c & 7], sv[c]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kHC; ++c) mx8[c & 7] = fmaxf(mx8[c & 7], sv[c]);
+        }
+        const float m_half = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                   fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * coef;
+        const float m_tile = fmaxf(m_half, exchange(m_half, ok));
+        if (!ok) break;
+        // the running maximum is raised only when it grows by more than 2^8 (or was empty)
+        float alpha = 1.f;
+        bool rescale_o = false;
+        if (m_tile > m_used + kRescaleThreshold || (m_used == -INFINITY && m_tile > -INFINITY)) {
+          if (m_used != -INFINITY) {
+            alpha = fast_exp2(m_used - m_tile);
+            l_part *= alpha;
+            rescale_o = true;
+          }
+          m_used = m_tile;
+        }
+        const float m_sub = (m_used == -INFINITY) ? 0.f : m_used;
+        uint32_t pk[kHC / 2];
+        float rs4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kHC / 2; ++c) {
+          const float p0 = fast_exp2(fmaf(sv[2 * c], coef, -m_sub));
+          const float p1 = fast_exp2(fmaf(sv[2 * c + 1], coef, -m_sub));
+          rs4[c & 3] += p0 + p1;
+          pk[c] = pack_bf16x2(p0, p1);
+        }
+        l_part += (rs4[0] + rs4[1]) + (rs4[2] + rs4[3]);
+        tmem_st_x32(tmem + lane_off + (b ? kColS1 : kColS0) + half * (kHC / 2), pk);
+        // O is rescaled by whole warps, once PV(t - 1) has finished; a unit's first tile never
+        // needs it. PV(t - 1) is the only phase of its barrier that can still be pending here.
+        const bool rescale_warp = __any_sync(0xffffffffu, rescale_o);
+        if (rescale_warp && jj >= 1) {
+          ok = __all_sync(0xffffffffu, wait_bar<PAIR>(&bars->pv_done[(t - 1) & 1], (uint32_t)((t - 1) >> 1) & 1u, abort_flag));
+          if (!ok) {
+            tmem_st_wait();
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < kHO / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_x32(tmem + lane_off + kColO + half * kHO + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st_x32(tmem + lane_off + kColO + half * kHO + c * 32, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (!PAIR || leader) mbar_arrive(&bars->p_full[b]);
+          else mbar_arrive_cluster(smem_u32(&bars->p_full[b]) & kPeerBitMask);
+        }
+      }
+      if (!ok) break;
+      const float l_sum = l_part + exchange(l_part, ok);
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu, wait_bar<PAIR>(&bars->o_ready, (uint32_t)unit_iter & 1u, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      const float inv_l = l_sum > 0.f ? 1.f / l_sum : l_sum == 0.f ? 0.f : l_sum;  // a NaN sum stays one
+      const bool cut = w.slot >= 0;
+      const bool wide = cut || a.out_f32;
+      const size_t orow = ((size_t)w.tok0 + tok) * a.hq + w.kvh * a.group + row_head;
+      // destination of this row's kDv columns: a cut unit's partial, or the output
+      uint8_t* dst = cut ? reinterpret_cast<uint8_t*>(p.part_o + (part_row * Cfg::kParts + w.part) * Cfg::kDv)
+                         : static_cast<uint8_t*>(a.out) + (orow * D + w.part * Cfg::kDv) * (a.out_f32 ? 4 : 2);
+      constexpr int kOC = kHO / 32;
+      constexpr int kOG = kOC >= 2 ? 2 : 1;
+#pragma unroll 1
+      for (int cg = 0; cg < kOC; cg += kOG) {
+        uint32_t ohg[kOG][32];
+#pragma unroll
+        for (int k = 0; k < kOG; ++k) tmem_ld_x32(tmem + lane_off + kColO + half * kHO + (cg + k) * 32, ohg[k]);
+        tmem_ld_wait();
+        if (cg + kOG >= kOC) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (!PAIR || leader) mbar_arrive(&bars->o_empty);
+            else mbar_arrive_cluster(smem_u32(&bars->o_empty) & kPeerBitMask);
+          }
+        }
+        if (!valid) continue;
+#pragma unroll
+        for (int k = 0; k < kOG; ++k) {
+          const uint32_t* oh = ohg[k];
+          const int col = half * kHO + (cg + k) * 32;
+          if (wide) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(dst + 4 * (col + 4 * i)) =
+                  make_float4(__uint_as_float(oh[4 * i]) * inv_l, __uint_as_float(oh[4 * i + 1]) * inv_l,
+                              __uint_as_float(oh[4 * i + 2]) * inv_l, __uint_as_float(oh[4 * i + 3]) * inv_l);
+          } else {
+            uint32_t wd[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              wd[i] = pack_bf16x2(__uint_as_float(oh[2 * i]) * inv_l, __uint_as_float(oh[2 * i + 1]) * inv_l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(dst + 2 * (col + 8 * i)) = make_uint4(wd[4 * i], wd[4 * i + 1], wd[4 * i + 2], wd[4 * i + 3]);
+          }
+        }
+      }
+      if (half == 0 && valid && w.part == 0) {
+        const float lse = l_sum > 0.f ? (m_used + log2f(l_sum)) * 0.6931471805599453f : l_sum == 0.f ? -INFINITY : l_sum;
+        if (cut) p.part_lse[part_row] = lse;
+        else if (a.lse != nullptr) a.lse[orow] = lse;
+      }
+      g += w.ntiles;
+      ++unit_iter;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) {  // a pair leaves together: no remote arrival or copy may target a CTA that has left
+    __syncwarp();
+    cluster_sync_all();
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, kTmemCols);
+    else tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Join of cut units: a warp takes 128 columns of one row, the pieces in order.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) chunk_merge_kernel(PagedAttendArgs a, ChunkPlan p) {
+  const int lane = threadIdx.x & 31;
+  const int D = a.c.d, chunks = (D + 127) / 128;
+  const int rows = p.rows, tpc = kCM / a.group;          // rows of a unit (128 per CTA), tokens per 128
+  const long long per_unit = (long long)a.c.hkv * rows * chunks;
+  const long long total = (long long)p.header[1] * per_unit;
+  for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += (long long)gridDim.x * 8) {
+    const int4 e = __ldg(p.merges + i / per_unit);  // sequence, unit, first slot, pieces
+    const int in_unit = (int)(i % per_unit);
+    const int c0 = (in_unit % chunks) * 128 + lane * 4;
+    const int row = (in_unit / chunks) % rows, kvh = in_unit / (chunks * rows);
+    const int cta = row / kCM, r = row % kCM, rt = r / a.group;
+    const int tok0 = __ldg(a.cu_q + e.x), n = __ldg(a.cu_q + e.x + 1) - tok0;
+    const int tok = e.y * p.tokens + cta * tpc + rt;
+    if (rt >= tpc || tok >= n) continue;
+    float mm = -INFINITY;
+    bool nan = false;
+    for (int s = 0; s < e.w; ++s) {
+      const float l = p.part_lse[((size_t)(e.z + s) * a.c.hkv + kvh) * rows + row];
+      nan |= l != l;
+      mm = fmaxf(mm, l);
+    }
+    float den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < e.w; ++s) {
+      const size_t pr = ((size_t)(e.z + s) * a.c.hkv + kvh) * rows + row;
+      const float l = p.part_lse[pr];
+      if (l == -INFINITY) continue;
+      const float w = nan ? l : __expf(l - mm);
+      den += w;
+      if (c0 < D) {
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + pr * D + c0);
+        acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
+      }
+    }
+    const size_t orow = ((size_t)tok0 + tok) * a.hq + kvh * a.group + (r - rt * a.group);
+    if (c0 < D) {
+      const float inv = den > 0.f || den != den ? 1.f / den : 0.f;
+      acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
+      const size_t o = orow * D + c0;
+      if (a.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = acc;
+      else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    }
+    if (c0 == 0 && a.lse) a.lse[orow] = den != den ? den : mm == -INFINITY ? -INFINITY : mm + logf(den);
+  }
+}
+
+template <int D, bool PAIR>
+static cudaError_t launch_chunk_t(const ChunkMaps& maps, const PagedAttendArgs& a, const ChunkPlan& p, int units_bound,
+                                  cudaStream_t stream) {
+  using Cfg = ChunkCfg<D, PAIR>;
+  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kCThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  if (PAIR) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  const int clusters = p.clusters < units_bound ? p.clusters : units_bound;
+  cfg.gridDim = dim3((unsigned)(clusters * (PAIR ? 2 : 1)));
+  return cudaLaunchKernelEx(&cfg, chunk_kernel<D, PAIR>, maps, a, p);
+}
+
+cudaError_t launch_chunk(const ChunkMaps& maps, const PagedAttendArgs& a, const ChunkPlan& p, int units_bound,
+                         cudaStream_t stream) {
+  chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, p);
+  if (p.e4m3) chunk_side_kernel<true><<<148 * 4, kSideThreads, 0, stream>>>(a, p);
+  else chunk_side_kernel<false><<<148 * 4, kSideThreads, 0, stream>>>(a, p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const bool pair = p.rows > kCM;
+  switch (a.c.d) {
+    case 64: e = launch_chunk_t<64, false>(maps, a, p, units_bound, stream); break;
+    case 128: e = pair ? launch_chunk_t<128, true>(maps, a, p, units_bound, stream) : launch_chunk_t<128, false>(maps, a, p, units_bound, stream); break;
+    case 256: e = pair ? launch_chunk_t<256, true>(maps, a, p, units_bound, stream) : launch_chunk_t<256, false>(maps, a, p, units_bound, stream); break;
+    case 512: e = pair ? launch_chunk_t<512, true>(maps, a, p, units_bound, stream) : launch_chunk_t<512, false>(maps, a, p, units_bound, stream); break;
+    default: return cudaErrorInvalidValue;
+  }
+  if (e != cudaSuccess) return e;
+  chunk_merge_kernel<<<148 * 2, 256, 0, stream>>>(a, p);
+  return cudaGetLastError();
+}
+
+}  // namespace gattn

@@ -140,7 +140,7 @@ __device__ __forceinline__ int blocks_per_split(const PagedAttendArgs& a, int la
   int longest = 1;
   for (int b = lane; b < a.batch; b += 32) {
     const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0, len = __ldg(a.lens + b);
-    if (n > 0 && seq_ok(a, tok0, n, len)) longest = max(longest, (len + n + kPB - 1) / kPB - keys_first(a, len, 0) / kPB);
+    if (n > 0 && !(a.chunk_of && a.chunk_of[b] >= 0) && seq_ok(a, tok0, n, len)) longest = max(longest, (len + n + kPB - 1) / kPB - keys_first(a, len, 0) / kPB);
   }
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, m));
@@ -151,7 +151,7 @@ __device__ __forceinline__ int blocks_per_split(const PagedAttendArgs& a, int la
   long long items = 0;
   for (int b = 0; b < a.batch; ++b) {
     const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0, len = __ldg(a.lens + b);
-    if (n <= 0 || !seq_ok(a, tok0, n, len)) continue;
+    if (n <= 0 || (a.chunk_of && a.chunk_of[b] >= 0) || !seq_ok(a, tok0, n, len)) continue;
     const int blocks = (len + n + kPB - 1) / kPB - keys_first(a, len, 0) / kPB;
     items += (long long)__float2int_ru((float)blocks * invT) * ((n * a.group + kPR - 1) / kPR);
   }
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
   const int b = (int)(idx / a.row_groups);
   const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0, len = __ldg(a.lens + b);
   const int R = n * a.group;                       // rows of this KV head
-  if (n == 0) return;
+  if (n == 0 || (a.chunk_of && a.chunk_of[b] >= 0)) return;
   if (!seq_ok(a, tok0, n, len)) {
     if (tid == 0 && split == 0 && rg == 0 && kvh == 0) atomicOr(&g_status, kStatusSeqlen);
     return;
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(PagedAttendArgs a) {
   if (tok >= __ldg(a.cu_q + a.batch)) return;
   const int b = seq_of_row(a.cu_q, a.batch, tok);
   const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0, len = __ldg(a.lens + b);
-  if (!seq_ok(a, tok0, n, len)) return;
+  if (!seq_ok(a, tok0, n, len) || (a.chunk_of && a.chunk_of[b] >= 0)) return;
   // the row's group of 8, as the attention kernel cut it
   const int r0 = ((tok - tok0) * a.group + head % a.group) / kPR * kPR;
   const int t0 = r0 / a.group, t1 = (min(r0 + kPR, n * a.group) - 1) / a.group;

@@ -330,8 +330,8 @@ int gemma_attn_combine(const float* partial_o, const float* partial_lse, int32_t
  *   block_table [batch, max_blocks] int32, device. Entries that no call's positions reach are
  *             never read, among them, for LOCAL, those of pages wholly before the oldest
  *             query's window: such pages may be reused. An entry that is read and lies outside
- *             [0, num_pages) records GEMMA_ATTN_ERR_PAGE; its keys are left out (attend), its
- *             rows not written (append), or zero (gather).
+ *             [0, num_pages) records GEMMA_ATTN_ERR_PAGE; its rows are then not written
+ *             (append), read as zero (gather), or make no statement (attend: that sequence's outputs).
  *   page_size 16, 32, 64, 128 or 256; num_pages * num_kv_heads < 2^31.
  * Page rows that hold no token yet, or a token outside every query's window, may hold anything,
  * NaN included. Among the rows that a call's queries do see, values must be finite: a row that
@@ -403,7 +403,9 @@ int gemma_attn_paged_workspace_size(const gemma_attn_params* params, const gemma
  *             sequence beyond either, or past max_blocks * page_size, records
  *             GEMMA_ATTN_ERR_SEQLEN and its rows are not written.
  *   workspace device buffer of gemma_attn_paged_workspace_size() bytes, 256-byte aligned;
- *             contents are scratch, nothing in it needs clearing. Calls that may run at the
+ *             contents are scratch, nothing in it needs clearing. For long chunks it holds
+ *             16-bit copies of what the tensor cores cannot read from the pages (GLOBAL: the
+ *             rotated dims of every key; E4M3: every row), so its size follows max_cache_len. Calls that may run at the
  *             same time (other streams, graphs replayed together) need one each.
  * Keys, probabilities and rotated rows enter the products in 16 bits; scores, softmax
  * statistics and outputs are accumulated in fp32. Over E4M3 pages the result is the attention
