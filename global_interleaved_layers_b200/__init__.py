@@ -248,22 +248,26 @@ def gemma_attn_tile_plan(kind: int, window: int, cu_seqlens_host, bm: int, bn: i
     return out[: int(n.value)]
 
 
-def _require(cond: bool, where: str, what: str) -> None:
-    if not cond:
-        e = GemmaAttnError(ERR_INVALID_ARG, where)
-        e.args = (f"{e.args[0]}: {what}",)
-        raise e
+def _refuse(where: str, what: str) -> None:
+    e = GemmaAttnError(ERR_INVALID_ARG, where)
+    e.args = (f"{e.args[0]}: {what}",)
+    raise e
 
 
-def _tensor(x, where: str, name: str, dtypes, shape=None, device=None):
-    """A torch tensor argument of a paged-cache or draft call: type, shape, layout and device are
-    checked (raw addresses and None pass)."""
-    if x is None or isinstance(x, int):
+def _tensor(x, where: str, name: str, dtype, shape=None, device=None):
+    """Address of a torch tensor argument of a paged-cache or draft call, after checks of its type, shape,
+    layout and device (raw addresses and None pass). A decode step makes a handful of these checks, so
+    messages are put together only on the way out."""
+    if x is None or type(x) is int:
         return x
-    _require(x.dtype in dtypes, where, f"{name} is {x.dtype}")
-    _require(x.is_contiguous(), where, f"{name} is not contiguous")
-    _require(shape is None or tuple(x.shape) == shape, where, f"{name} has shape {tuple(x.shape)}, not {shape}")
-    _require(device is None or x.device == device, where, f"{name} is on {x.device}, not {device}")
+    if x.dtype is not dtype:
+        _refuse(where, f"{name} is {x.dtype}, not {dtype}")
+    if not x.is_contiguous():
+        _refuse(where, f"{name} is not contiguous")
+    if shape is not None and x.shape != shape:
+        _refuse(where, f"{name} has shape {tuple(x.shape)}, not {shape}")
+    if device is not None and x.device != device:
+        _refuse(where, f"{name} is on {x.device}, not {device}")
     return x.data_ptr()
 
 
@@ -273,54 +277,57 @@ def paged_cache(k_pages, v_pages, block_table, k_scales=None, v_scales=None) -> 
     with float32 scales [num_pages, kv_heads, page_size]; block_table [batch, max_blocks] int32."""
     import torch
     where = "paged_cache"
-    _require(k_pages.dim() == 4 and block_table.dim() == 2, where, "k_pages has 4 dimensions, block_table 2")
+    if k_pages.dim() != 4 or block_table.dim() != 2:
+        _refuse(where, "k_pages has 4 dimensions, block_table 2")
+    if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        _refuse(where, f"k_pages is {k_pages.dtype}")
     e4m3 = k_pages.dtype == torch.float8_e4m3fn
+    if e4m3 != (k_scales is not None) or (e4m3 and v_pages is not None) != (v_scales is not None):
+        _refuse(where, "float8_e4m3fn pages have scales, bfloat16 pages none")
     dev, shape = k_pages.device, tuple(k_pages.shape)
-    k = _tensor(k_pages, where, "k_pages", (torch.bfloat16, torch.float8_e4m3fn))
-    v = _tensor(v_pages, where, "v_pages", (k_pages.dtype,), shape, dev)
-    _require(e4m3 == (k_scales is not None) and (e4m3 and v_pages is not None) == (v_scales is not None), where,
-             "float8_e4m3fn pages have scales, bfloat16 pages none")
-    ks = _tensor(k_scales, where, "k_scales", (torch.float32,), shape[:3], dev)
-    vs = _tensor(v_scales, where, "v_scales", (torch.float32,), shape[:3], dev)
-    tab = _tensor(block_table, where, "block_table", (torch.int32,), None, dev)
+    k = _tensor(k_pages, where, "k_pages", k_pages.dtype)
+    v = _tensor(v_pages, where, "v_pages", k_pages.dtype, shape, dev)
+    ks = _tensor(k_scales, where, "k_scales", torch.float32, shape[:3], dev)
+    vs = _tensor(v_scales, where, "v_scales", torch.float32, shape[:3], dev)
+    tab = _tensor(block_table, where, "block_table", torch.int32, None, dev)
     c = GemmaAttnPagedCache(k, v, ks, vs, tab, shape[0], shape[2], block_table.shape[1],
                             PAGES_E4M3 if e4m3 else PAGES_BF16)
     c.tensors = (k_pages, v_pages, block_table, k_scales, v_scales)
+    c.fits = (shape[1], shape[3], block_table.shape[0], dev)
     return c
 
 
-class _On:
-    """The device of a call's tensors made current, and the stream to launch on (by default that
-    device's current one)."""
-
-    def __init__(self, device, stream):
-        self.device, self.stream, self.old = device, stream, None
-
-    def __enter__(self):
-        import torch
-        if self.device is not None and self.device.type == "cuda":
-            now = torch.cuda.current_device()
-            if now != self.device.index:
-                self.old = now
-                torch.cuda.set_device(self.device)
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.old is not None:
-            import torch
-            torch.cuda.set_device(self.old)
+def _call(fn, where: str, device, stream, *args) -> None:
+    """fn(*args, stream) with `device` (of the call's tensors, or None) current; by default the stream
+    is that device's current one."""
+    if device is None or device.type != "cuda":
+        _check(fn(*args, _stream(stream)), where)
+        return
+    import torch
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)), where)
+        return
+    if stream is None:
+        st = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        st = stream if type(stream) is int else stream.cuda_stream
+    rc = fn(*args, st)
+    if rc != OK:
+        raise GemmaAttnError(rc, where)
 
 
 def _cache_fits(p: GemmaAttnParams, cache: GemmaAttnPagedCache, batch: int, where: str):
     """The handle's tensors (when it was made from tensors) against the layer; returns their device."""
-    tensors = getattr(cache, "tensors", None)
-    if tensors is None:
+    fits = getattr(cache, "fits", None)
+    if fits is None:
         return None
-    kp, _, table = tensors[:3]
-    _require(kp.shape[1] == p.num_kv_heads and kp.shape[3] == p.head_dim, where,
-             f"k_pages has {kp.shape[1]} heads of {kp.shape[3]} dims, the layer {p.num_kv_heads} of {p.head_dim}")
-    _require(table.shape[0] >= batch, where, f"block_table has {table.shape[0]} rows for {batch} sequences")
-    return kp.device
+    heads, dim, rows, dev = fits
+    if heads != p.num_kv_heads or dim != p.head_dim:
+        _refuse(where, f"k_pages has {heads} heads of {dim} dims, the layer {p.num_kv_heads} of {p.head_dim}")
+    if rows < batch:
+        _refuse(where, f"block_table has {rows} rows for {batch} sequences")
+    return dev
 
 
 def gemma_attn_paged_append(p: GemmaAttnParams, cache: GemmaAttnPagedCache, new_k, new_v, cu_q, cache_seqlens,
@@ -330,13 +337,11 @@ def gemma_attn_paged_append(p: GemmaAttnParams, cache: GemmaAttnPagedCache, new_
     where = "gemma_attn_paged_append"
     dev = _cache_fits(p, cache, batch, where)
     shape = (total_q, p.num_kv_heads, p.head_dim)
-    k = _tensor(new_k, where, "new_k", (torch.bfloat16,), shape, dev)
-    v = _tensor(new_v, where, "new_v", (torch.bfloat16,), shape, dev)
-    cu = _tensor(cu_q, where, "cu_q", (torch.int32,), (batch + 1,), dev)
-    lens = _tensor(cache_seqlens, where, "cache_seqlens", (torch.int32,), (batch,), dev)
-    with _On(dev, stream) as st:
-        _check(_lib.gemma_attn_paged_append(ctypes.byref(p), ctypes.byref(cache), k, v, cu, lens, batch, total_q, st),
-               where)
+    _call(_lib.gemma_attn_paged_append, where, dev, stream, ctypes.byref(p), ctypes.byref(cache),
+          _tensor(new_k, where, "new_k", torch.bfloat16, shape, dev),
+          _tensor(new_v, where, "new_v", torch.bfloat16, shape, dev),
+          _tensor(cu_q, where, "cu_q", torch.int32, (batch + 1,), dev),
+          _tensor(cache_seqlens, where, "cache_seqlens", torch.int32, (batch,), dev), batch, total_q)
 
 
 def gemma_attn_paged_gather(p: GemmaAttnParams, cache: GemmaAttnPagedCache, starts, cu_out, out_k, out_v, batch: int,
@@ -346,14 +351,12 @@ def gemma_attn_paged_gather(p: GemmaAttnParams, cache: GemmaAttnPagedCache, star
     where = "gemma_attn_paged_gather"
     dev = _cache_fits(p, cache, batch, where)
     shape = (total_out, p.num_kv_heads, p.head_dim)
-    dt = (torch.float32 if p.out_dtype == OUT_F32 else torch.bfloat16,)
-    k = _tensor(out_k, where, "out_k", dt, shape, dev)
-    v = _tensor(out_v, where, "out_v", dt, shape, dev)
-    first = _tensor(starts, where, "starts", (torch.int32,), (batch,), dev)
-    cu = _tensor(cu_out, where, "cu_out", (torch.int32,), (batch + 1,), dev)
-    with _On(dev, stream) as st:
-        _check(_lib.gemma_attn_paged_gather(ctypes.byref(p), ctypes.byref(cache), first, cu, k, v, batch, total_out, st),
-               where)
+    dt = torch.float32 if p.out_dtype == OUT_F32 else torch.bfloat16
+    _call(_lib.gemma_attn_paged_gather, where, dev, stream, ctypes.byref(p), ctypes.byref(cache),
+          _tensor(starts, where, "starts", torch.int32, (batch,), dev),
+          _tensor(cu_out, where, "cu_out", torch.int32, (batch + 1,), dev),
+          _tensor(out_k, where, "out_k", dt, shape, dev), _tensor(out_v, where, "out_v", dt, shape, dev), batch,
+          total_out)
 
 
 def gemma_attn_paged_workspace_size(p: GemmaAttnParams, cache: GemmaAttnPagedCache, batch: int, total_q: int,
@@ -372,17 +375,18 @@ def gemma_attn_paged_attend(p: GemmaAttnParams, cache: GemmaAttnPagedCache, q, c
     where = "gemma_attn_paged_attend"
     dev = _cache_fits(p, cache, batch, where)
     shape = (total_q, p.num_q_heads, p.head_dim)
-    qp = _tensor(q, where, "q", (torch.bfloat16,), shape, dev)
-    o = _tensor(out, where, "out", (torch.float32 if p.out_dtype == OUT_F32 else torch.bfloat16,), shape, dev)
-    ls = _tensor(lse, where, "lse", (torch.float32,), shape[:2], dev)
-    cu = _tensor(cu_q, where, "cu_q", (torch.int32,), (batch + 1,), dev)
-    lens = _tensor(cache_seqlens, where, "cache_seqlens", (torch.int32,), (batch,), dev)
-    if hasattr(workspace, "data_ptr"):
-        _require(workspace.is_contiguous() and workspace.numel() * workspace.element_size() >= workspace_bytes
-                 and (dev is None or workspace.device == dev), where, "workspace is not workspace_bytes on the cache's device")
-    with _On(dev, stream) as st:
-        _check(_lib.gemma_attn_paged_attend(ctypes.byref(p), ctypes.byref(cache), qp, cu, lens, o, ls, batch, total_q,
-                                            max_q, max_cache_len, _ptr(workspace), workspace_bytes, st), where)
+    ws = workspace
+    if ws is not None and type(ws) is not int:
+        if not ws.is_contiguous() or ws.numel() * ws.element_size() < workspace_bytes or dev not in (None, ws.device):
+            _refuse(where, "workspace is not workspace_bytes of the cache's device")
+        ws = ws.data_ptr()
+    _call(_lib.gemma_attn_paged_attend, where, dev, stream, ctypes.byref(p), ctypes.byref(cache),
+          _tensor(q, where, "q", torch.bfloat16, shape, dev),
+          _tensor(cu_q, where, "cu_q", torch.int32, (batch + 1,), dev),
+          _tensor(cache_seqlens, where, "cache_seqlens", torch.int32, (batch,), dev),
+          _tensor(out, where, "out", torch.float32 if p.out_dtype == OUT_F32 else torch.bfloat16, shape, dev),
+          _tensor(lse, where, "lse", torch.float32, shape[:2], dev), batch, total_q, max_q, max_cache_len, ws,
+          workspace_bytes)
 
 
 def gemma_attn_draft_verify(target_probs, draft_probs, draft_tokens, draft_lens, uniforms, noise, num_accepted,
@@ -393,21 +397,19 @@ def gemma_attn_draft_verify(target_probs, draft_probs, draft_tokens, draft_lens,
     num_accepted [batch] and out_tokens [batch, max_draft + 1] int32 are written."""
     import torch
     where = "gemma_attn_draft_verify"
-    _require(target_probs.dim() == 3, where, "target_probs has 3 dimensions")
+    dt = target_probs.dtype
+    if target_probs.dim() != 3 or target_probs.shape[1] < 1 or dt not in (torch.float32, torch.bfloat16):
+        _refuse(where, "target_probs is [batch, max_draft + 1, vocab], float32 or bfloat16")
     b, n1, v = target_probs.shape
-    _require(n1 >= 1, where, "target_probs holds max_draft + 1 rows")
-    dev, dt, i32, f32 = target_probs.device, target_probs.dtype, (torch.int32,), (torch.float32,)
-    tp = _tensor(target_probs, where, "target_probs", (torch.float32, torch.bfloat16))
-    dp = _tensor(draft_probs, where, "draft_probs", (dt,), (b, n1 - 1, v), dev)
-    tok = _tensor(draft_tokens, where, "draft_tokens", i32, (b, n1 - 1), dev)
-    lens = _tensor(draft_lens, where, "draft_lens", i32, (b,), dev)
-    uni = _tensor(uniforms, where, "uniforms", f32, (b, n1 - 1), dev)
-    nz = _tensor(noise, where, "noise", f32, (b, v), dev)
-    acc = _tensor(num_accepted, where, "num_accepted", i32, (b,), dev)
-    out = _tensor(out_tokens, where, "out_tokens", i32, (b, n1), dev)
-    with _On(dev, stream) as st:
-        _check(_lib.gemma_attn_draft_verify(tp, dp, PROBS_BF16 if dt == torch.bfloat16 else PROBS_F32, tok, lens, uni,
-                                            nz, b, n1 - 1, v, acc, out, st), where)
+    dev, i32, f32 = target_probs.device, torch.int32, torch.float32
+    _call(_lib.gemma_attn_draft_verify, where, dev, stream, _tensor(target_probs, where, "target_probs", dt),
+          _tensor(draft_probs, where, "draft_probs", dt, (b, n1 - 1, v), dev),
+          PROBS_BF16 if dt == torch.bfloat16 else PROBS_F32,
+          _tensor(draft_tokens, where, "draft_tokens", i32, (b, n1 - 1), dev),
+          _tensor(draft_lens, where, "draft_lens", i32, (b,), dev),
+          _tensor(uniforms, where, "uniforms", f32, (b, n1 - 1), dev), _tensor(noise, where, "noise", f32, (b, v), dev),
+          b, n1 - 1, v, _tensor(num_accepted, where, "num_accepted", i32, (b,), dev),
+          _tensor(out_tokens, where, "out_tokens", i32, (b, n1), dev))
 
 
 def gemma_attn_check(stream=None) -> None:

@@ -6,9 +6,24 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace gattn {
+
+// Allow `kernel` `bytes` of dynamic shared memory on the current device, once per device.
+template <typename F>
+cudaError_t allow_smem(F kernel, int bytes, std::atomic<bool>* ready /* [64] */) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready[dev].store(true, std::memory_order_release);
+  return e;
+}
 
 enum : int { kStatusPage = 4 };  // device status word: a block-table entry outside the pool
 
@@ -84,16 +99,25 @@ struct PagedAttendArgs {
   int r;                    // rotated pairs
   double log2_base;
   float softmax_scale;
-  // row-group kernel: split partials
-  float* partial_o;         // [splits, T * Hq, d]
-  float* partial_lse;       // [splits, T * Hq]
-  int splits;               // most splits of a sequence's keys
-  int row_groups;           // groups of 8 rows (query, head of the KV head's group) of the longest chunk
+  // row-group kernel: parts of cut units, two a team
+  float* partial_o;         // [2 teams, 8, d]
+  float* partial_lse;       // [2 teams, 8]
+  int row_groups;           // most groups of 8 rows (query, head of the KV head's group) of a sequence
   const int* chunk_of;      // [batch], >= 0: the sequence is chunk_kernel's; null: there are none
+  int cut, teams, run_step; // set at the launch: units are cut into equal runs; teams; a run is a multiple of run_step
 };
-// Split-KV attention of 8 rows per warp-set over pages (paged_decode.cu), and its merge.
-cudaError_t launch_paged_rows(const PagedAttendArgs& a, bool e4m3, cudaStream_t stream);
-int paged_rows_splits(int batch, int hkv, int row_groups, int max_keys);
+
+constexpr int kSms = 148;
+
+// How the row-group kernel (paged_decode.cu) runs a call.
+struct PagedRowsShape {
+  int warp_teams;           // units go to single warps, not CTAs
+  int cut;
+  int q_rows;               // rows of the fullest group
+  int nw, nsk, nsv;         // warps of a CTA; key (K=V) and value stages of a warp's ring
+};
+PagedRowsShape paged_rows_shape(int head_dim, bool local, long long units, long long max_blocks, int group_rows);
+cudaError_t launch_paged_rows(const PagedAttendArgs& a, const PagedRowsShape& f, bool e4m3, cudaStream_t stream);
 
 // Long chunks (paged_chunk.cu): the device-side plan and the buffers it names, all in the
 // call's workspace.

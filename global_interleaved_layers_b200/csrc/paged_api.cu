@@ -51,7 +51,8 @@ constexpr int kChunkMinRows = 64;
 
 // How an attend call's work is cut, and what of the workspace each part takes (byte offsets).
 struct AttendPlan {
-  int row_groups, splits;           // row-group kernel
+  int row_groups;                   // row-group kernel
+  PagedRowsShape shape;
   size_t part_o, part_lse;
   bool chunk;                       // some sequence may have more rows than kChunkMinRows
   bool pair;
@@ -79,10 +80,12 @@ int attend_plan(const gemma_attn_params* p, bool e4m3, int batch, int total_q, i
   const long long keys = local ? std::min<long long>(max_cache_len, p->window) + max_q : (long long)max_cache_len + max_q;
   L->chunk = (long long)max_q * group > kChunkMinRows;
   L->row_groups = L->chunk ? kChunkMinRows / 8 : (max_q * group + 7) / 8;
-  L->splits = paged_rows_splits(batch, hkv, std::max(1, L->row_groups), (int)keys);
-  if (L->splits > 1) {
-    L->part_o = take((size_t)L->splits * rows * d * 4);
-    L->part_lse = take((size_t)L->splits * rows * 4);
+  L->shape = paged_rows_shape(d, local, (long long)batch * hkv * std::max(1, L->row_groups), (keys + 15) / 16 + 1,
+                              L->chunk ? 8 : max_q * group);
+  if (L->shape.cut) {
+    const int parts = 2 * kSms * (L->shape.warp_teams ? 8 : 1);  // two a team
+    L->part_o = take((size_t)parts * 8 * d * 4);
+    L->part_lse = take((size_t)parts * 8 * 4);
   }
   if (L->chunk) {
     const int r = rotated_pairs(p->rope_p, d);
@@ -291,12 +294,11 @@ int gemma_attn_paged_attend(const gemma_attn_params* params, const gemma_attn_pa
   a.log2_base = log2((double)params->rope_base);
   a.softmax_scale = params->softmax_scale;
   a.row_groups = plan.row_groups;
-  a.splits = plan.splits;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.partial_o = reinterpret_cast<float*>(ws + plan.part_o);
   a.partial_lse = reinterpret_cast<float*>(ws + plan.part_lse);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int launches = plan.splits > 1 ? 2 : 1;
+  int launches = plan.shape.cut ? 2 : 1;
   if (plan.chunk) {
     if (plan.seqs > 0) {
       a.chunk_of = reinterpret_cast<int*>(ws + plan.chunk_of);
@@ -305,7 +307,7 @@ int gemma_attn_paged_attend(const gemma_attn_params* params, const gemma_attn_pa
       launches += 4;
     }
   }
-  return launched(launch_paged_rows(a, e4m3, s), launches);
+  return launched(launch_paged_rows(a, plan.shape, e4m3, s), launches);
 }
 
 int gemma_attn_draft_verify(const void* target_probs, const void* draft_probs, int32_t prob_dtype,

@@ -955,7 +955,8 @@ template <int D, bool PAIR>
 static cudaError_t launch_chunk_t(const ChunkMaps& maps, const PagedAttendArgs& a, const ChunkPlan& p, int units_bound,
                                   cudaStream_t stream) {
   using Cfg = ChunkCfg<D, PAIR>;
-  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+  static std::atomic<bool> ready[64];
+  const cudaError_t e = allow_smem(chunk_kernel<D, PAIR>, Cfg::kSmemBytes, ready);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kCThreads);
