@@ -12,6 +12,16 @@
 
 namespace gattn {
 
+// One lane of a converged warp. tcgen05.mma takes its descriptors from uniform registers: behind
+// this predicate the compiler knows that one thread runs and moves them there directly, behind
+// `lane == 0` it adds a loop over the active lanes to every MMA (measured per 128 x 16 x 16 MMA:
+// 51 cycles against 111 to 204).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{.reg .pred q; elect.sync _|q, 0xffffffff; selp.u32 %0, 1, 0, q;}" : "=r"(p));
+  return p != 0;
+}
+
 // Allow `kernel` `bytes` of dynamic shared memory on the current device, once per device.
 template <typename F>
 cudaError_t allow_smem(F kernel, int bytes, std::atomic<bool>* ready /* [64] */) {
@@ -104,20 +114,29 @@ struct PagedAttendArgs {
   float* partial_lse;       // [2 teams, 8]
   int row_groups;           // most groups of 8 rows (query, head of the KV head's group) of a sequence
   const int* chunk_of;      // [batch], >= 0: the sequence is chunk_kernel's; null: there are none
-  int cut, teams, run_step; // set at the launch: units are cut into equal runs; teams; a run is a multiple of run_step
+  // set at the launch: units are cut into equal runs; teams; a run is a multiple of run_step;
+  // rows of a unit (8 or 40), log2 of the keys of a block
+  int cut, teams, run_step, unit_rows, unit_shift;
 };
 
 constexpr int kSms = 148;
 
-// How the row-group kernel (paged_decode.cu) runs a call.
+// How a call's short sequences run.
 struct PagedRowsShape {
+  int tile;                 // the tensor-core kernel (paged_tile.cu), not the one below
+  int unit_rows, row_groups;
+  int cut;                  // units are cut into equal runs
+  int parts;                // places for parts of cut units
+  // row-group kernel (paged_decode.cu)
   int warp_teams;           // units go to single warps, not CTAs
-  int cut;
   int q_rows;               // rows of the fullest group
   int nw, nsk, nsv;         // warps of a CTA; key (K=V) and value stages of a warp's ring
 };
-PagedRowsShape paged_rows_shape(int head_dim, bool local, long long units, long long max_blocks, int group_rows);
+// `rows` rows per KV head and `keys` visible keys at most.
+PagedRowsShape paged_rows_shape(int head_dim, bool local, int rotated, int batch, int hkv, int rows, long long keys);
 cudaError_t launch_paged_rows(const PagedAttendArgs& a, const PagedRowsShape& f, bool e4m3, cudaStream_t stream);
+cudaError_t launch_paged_tile(const PagedAttendArgs& a, const PagedRowsShape& f, bool e4m3, cudaStream_t stream);
+cudaError_t launch_paged_merge(const PagedAttendArgs& a, cudaStream_t stream);
 
 // Long chunks (paged_chunk.cu): the device-side plan and the buffers it names, all in the
 // call's workspace.

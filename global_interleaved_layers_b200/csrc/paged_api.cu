@@ -51,8 +51,7 @@ constexpr int kChunkMinRows = 64;
 
 // How an attend call's work is cut, and what of the workspace each part takes (byte offsets).
 struct AttendPlan {
-  int row_groups;                   // row-group kernel
-  PagedRowsShape shape;
+  PagedRowsShape shape;             // the sequences that are not chunks
   size_t part_o, part_lse;
   bool chunk;                       // some sequence may have more rows than kChunkMinRows
   bool pair;
@@ -79,16 +78,13 @@ int attend_plan(const gemma_attn_params* p, bool e4m3, int batch, int total_q, i
   };
   const long long keys = local ? std::min<long long>(max_cache_len, p->window) + max_q : (long long)max_cache_len + max_q;
   L->chunk = (long long)max_q * group > kChunkMinRows;
-  L->row_groups = L->chunk ? kChunkMinRows / 8 : (max_q * group + 7) / 8;
-  L->shape = paged_rows_shape(d, local, (long long)batch * hkv * std::max(1, L->row_groups), (keys + 15) / 16 + 1,
-                              L->chunk ? 8 : max_q * group);
+  const int r = rotated_pairs(p->rope_p, d);
+  L->shape = paged_rows_shape(d, local, r, batch, hkv, L->chunk ? kChunkMinRows : std::max(1, max_q * group), keys);
   if (L->shape.cut) {
-    const int parts = 2 * kSms * (L->shape.warp_teams ? 8 : 1);  // two a team
-    L->part_o = take((size_t)parts * 8 * d * 4);
-    L->part_lse = take((size_t)parts * 8 * 4);
+    L->part_o = take((size_t)L->shape.parts * L->shape.unit_rows * d * 4);
+    L->part_lse = take((size_t)L->shape.parts * L->shape.unit_rows * 4);
   }
   if (L->chunk) {
-    const int r = rotated_pairs(p->rope_p, d);
     L->q_mask = rotated_chunk_mask(d, r);
     L->k_mask = local ? 0u : L->q_mask;
     L->pair = d >= 128 && (long long)max_q * group > 128;
@@ -293,7 +289,7 @@ int gemma_attn_paged_attend(const gemma_attn_params* params, const gemma_attn_pa
   a.r = rotated_pairs(params->rope_p, params->head_dim);
   a.log2_base = log2((double)params->rope_base);
   a.softmax_scale = params->softmax_scale;
-  a.row_groups = plan.row_groups;
+  a.row_groups = plan.shape.row_groups;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.partial_o = reinterpret_cast<float*>(ws + plan.part_o);
   a.partial_lse = reinterpret_cast<float*>(ws + plan.part_lse);

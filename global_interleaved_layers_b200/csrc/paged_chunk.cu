@@ -605,7 +605,7 @@ chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ Pag
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (lane == 0 && leader) {
+    if (leader && elect_one()) {
       constexpr int M = PAIR ? 2 * kCM : kCM;
       constexpr int PV_N = Cfg::kPvN;
       const uint32_t idesc_qk = umma_idesc_bf16(M, kCN, 0, 0);

@@ -132,31 +132,40 @@ __device__ __forceinline__ bool seq_ok(const PagedAttendArgs& a, int tok0, int n
          (long long)len + n <= ((long long)a.c.max_blocks << a.c.page_shift);
 }
 
+// ceil(rows / unit_rows) for unit_rows 8 or 40: an eighth, and a fifth of that by its reciprocal.
+__device__ __forceinline__ int row_groups_of(int rows, int unit_rows) {
+  const uint32_t e = (uint32_t)(rows + unit_rows - 1) >> 3;
+  return unit_rows == 8 ? e : __umulhi(e, 0xCCCCCCCDu) >> 2;
+}
+
 // Blocks of each unit of sequence b and its number of units; both 0 when it is not served here.
-__device__ __forceinline__ void seq_units(const PagedAttendArgs& a, int b, int* blocks, int* units) {
+// (Out of line, as everything that runs once per unit: a kernel's loops should stay in the
+// instruction caches.)
+__device__ __noinline__ void seq_units(const PagedAttendArgs& a, int b, int* blocks, int* units) {
   *blocks = *units = 0;
   if (b >= a.batch) return;
   const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0, len = __ldg(a.lens + b);
   if (n <= 0 || (a.chunk_of && a.chunk_of[b] >= 0) || !seq_ok(a, tok0, n, len)) return;
-  *blocks = (len + n + kPB - 1) / kPB - keys_first(a, len, 0) / kPB;
-  *units = min((n * a.group + kPR - 1) / kPR, a.row_groups) * a.c.hkv;
+  *blocks = ((len + n + (1 << a.unit_shift) - 1) >> a.unit_shift) - (keys_first(a, len, 0) >> a.unit_shift);
+  *units = min(row_groups_of(n * a.group, a.unit_rows), a.row_groups) * a.c.hkv;
 }
 
 // By one warp: the total over all sequences of their units (cut = 0) or of their units' blocks,
 // and the sequence that holds element `x` of that line, with the total before it. Sequence
-// batch when there is none.
-__device__ __forceinline__ long long line_find(const PagedAttendArgs& a, int lane, long long x, int* seq, long long* before) {
-  long long total = 0;
+// batch when there is none. (In 32 bits: launch_paged_rows refuses longer lines.)
+__device__ __noinline__ int line_find(const PagedAttendArgs& a, int lane, int x, int* seq, int* before) {
+  int total = 0;
   *seq = a.batch;
   *before = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     int blocks, units;
     seq_units(a, b0 + lane, &blocks, &units);
-    const long long w = a.cut ? (long long)blocks * units : units;
-    long long incl = w;
-#pragma unroll
+    const int w = a.cut ? blocks * units : units;
+    int incl = w;
+#pragma unroll 1
     for (int m = 1; m < 32; m <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, incl, m);
+      const int o = __shfl_up_sync(0xffffffffu, incl, m);
       if (lane >= m) incl += o;
     }
     const uint32_t here = __ballot_sync(0xffffffffu, x >= total + incl - w && x < total + incl);
@@ -170,11 +179,11 @@ __device__ __forceinline__ long long line_find(const PagedAttendArgs& a, int lan
   return total;
 }
 
-// Length of a team's run of the line, `nteams` teams.
-__device__ __forceinline__ long long run_length(const PagedAttendArgs& a, long long total) {
+// Length of a team's run of the line.
+__device__ __forceinline__ int run_length(const PagedAttendArgs& a, int total) {
   if (!a.cut) return 1;
-  const long long per = (total + a.teams - 1) / a.teams;
-  return (per + a.run_step - 1) / a.run_step * a.run_step;
+  const uint32_t per = ((uint32_t)total + a.teams - 1) / (uint32_t)a.teams;
+  return (int)((per + a.run_step - 1) / (uint32_t)a.run_step * a.run_step);
 }
 
 }  // namespace
@@ -246,15 +255,13 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
   __syncthreads();
 
   // ---- this team's run [x, x_end) of the line of blocks (cut) or units
-  const long long team = WARP_TEAMS ? (long long)blockIdx.x * NW + warp : blockIdx.x;
-  int b;
-  long long before;
-  long long x = 0, x_end = 0;
+  const int team = WARP_TEAMS ? (int)blockIdx.x * NW + warp : (int)blockIdx.x;
+  int b, before, x, x_end;
   {
-    const long long total = line_find(a, lane, a.cut ? -1 : team, &b, &before);
-    const long long run = run_length(a, total);
-    x = team * run;
-    x_end = a.cut ? min(total, x + run) : total;   // uncut: units team, team + teams, ...
+    const int total = line_find(a, lane, a.cut ? -1 : team, &b, &before);
+    const int run = run_length(a, total);
+    x = min((long long)team * run, (long long)total);
+    x_end = a.cut ? (int)min((long long)total, (long long)x + run) : total;   // uncut: units team, team + teams, ...
     if (x < x_end && a.cut) line_find(a, lane, x, &b, &before);
   }
 
@@ -267,13 +274,13 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
     // ---- the piece: blocks [b_lo, b_hi) of one unit
     int blocks, units;
     seq_units(a, b, &blocks, &units);
-    if (x - before >= (a.cut ? (long long)blocks * units : units)) {  // past this sequence
+    if (x - before >= (a.cut ? blocks * units : units)) {  // past this sequence
       line_find(a, lane, x, &b, &before);
       seq_units(a, b, &blocks, &units);
     }
-    const int u = (int)(a.cut ? (x - before) / blocks : x - before);
-    const int b_lo = a.cut ? (int)((x - before) % blocks) : 0;
-    const int b_hi = a.cut ? (int)min((long long)blocks, x_end - x + b_lo) : blocks;
+    const int u = a.cut ? (x - before) / blocks : x - before;
+    const int b_lo = a.cut ? (x - before) % blocks : 0;
+    const int b_hi = a.cut ? min(blocks, x_end - x + b_lo) : blocks;
     const int kvh = u % a.c.hkv, row0 = u / a.c.hkv * kPR;
     const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0, len = __ldg(a.lens + b);
     const int rows = min(kPR, n * a.group - row0);
@@ -822,26 +829,26 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(PagedAttendArgs a) {
   seq_units(a, b, &blocks, &units);
   if (units == 0) return;
   // units and blocks before this sequence, and in all
-  long long before = 0, total = 0;
+  int before = 0, total = 0;
   for (int i = lane; i < a.batch; i += 32) {
     int bl, un;
     seq_units(a, i, &bl, &un);
-    total += (long long)bl * un;
-    if (i < b) before += (long long)bl * un;
+    total += bl * un;
+    if (i < b) before += bl * un;
   }
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) {
     total += __shfl_xor_sync(0xffffffffu, total, m);
     before += __shfl_xor_sync(0xffffffffu, before, m);
   }
-  const long long run = run_length(a, total);
+  const int run = run_length(a, total);
   const int in_head = (tok - __ldg(a.cu_q + b)) * a.group + head % a.group;  // row within the KV head
-  const int u = in_head / kPR * a.c.hkv + head / a.group;
+  const int ur = a.unit_rows, u = in_head / ur * a.c.hkv + head / a.group;
   if (u >= units) return;
-  const long long x0 = before + (long long)u * blocks, x1 = x0 + blocks;
-  const int w0 = (int)(x0 / run), w1 = (int)((x1 - 1) / run);
+  const int x0 = before + u * blocks, x1 = x0 + blocks;
+  const int w0 = x0 / run, w1 = (x1 - 1) / run;
   if (w0 == w1) return;  // one team had it all, and wrote the output
-  auto at = [&](int w) { return ((size_t)2 * w + (w == w0 ? 1 : 0)) * kPR + in_head % kPR; };
+  auto at = [&](int w) { return ((size_t)2 * w + (w == w0 ? 1 : 0)) * ur + in_head % ur; };
   float mm = -INFINITY;
   bool nan = false;
   for (int w = w0 + lane; w <= w1; w += 32) {
@@ -875,14 +882,35 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(PagedAttendArgs a) {
   if (c0 == 0 && a.lse) a.lse[row] = den != den ? den : mm == -INFINITY ? -INFINITY : mm + logf(den);
 }
 
+cudaError_t launch_paged_merge(const PagedAttendArgs& a, cudaStream_t stream) {
+  const long long warps = (long long)a.total_q * a.hq * ((a.c.d + 127) / 128);
+  paged_merge_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
 // Teams for a call: `units` units of at most `max_blocks` blocks, `group_rows` rows in a group.
 //   Single warps from four units per SM on (head dims to 256, whose query rows fit beside eight
 //   rings). Uncut where every unit may go whole: short ones (each of a CTA's warps takes four
 //   blocks or fewer: cutting would only add the merge), or window-sized ones that fill the warps'
 //   rounds to 80 percent.
-PagedRowsShape paged_rows_shape(int head_dim, bool local, long long units, long long max_blocks, int group_rows) {
+//   The tensor-core kernel (paged_tile.cu) takes what it can: head dims from 128, at most 64
+//   rotated pairs of K=V keys.
+PagedRowsShape paged_rows_shape(int head_dim, bool local, int rotated, int batch, int hkv, int rows, long long keys) {
   PagedRowsShape f{};
-  f.q_rows = std::min(kPR, group_rows);
+  if (head_dim >= 128 && (local || rotated <= 64)) {
+    f.tile = 1;
+    f.unit_rows = rows <= 8 ? 8 : 40;
+    f.row_groups = std::max(1, (rows + f.unit_rows - 1) / f.unit_rows);
+    const long long units = (long long)batch * hkv * f.row_groups;
+    const long long tiles = keys / 64 + 2, rounds = (units + kSms - 1) / kSms;
+    f.cut = tiles > 6 && !(local && units * 5 >= rounds * kSms * 4);
+    f.parts = 2 * kSms;
+    return f;
+  }
+  f.unit_rows = kPR;
+  f.row_groups = std::max(1, (rows + kPR - 1) / kPR);
+  f.q_rows = std::min(kPR, rows);
+  const long long units = (long long)batch * hkv * f.row_groups, max_blocks = (keys + kPB - 1) / kPB + 1;
   f.warp_teams = head_dim <= 256 && units >= 4 * kSms ? 1 : 0;
   const long long warps = 8ll * kSms;
   if (f.warp_teams) {
@@ -891,6 +919,7 @@ PagedRowsShape paged_rows_shape(int head_dim, bool local, long long units, long 
   } else {
     f.cut = max_blocks > 32;
   }
+  f.parts = 2 * kSms * (f.warp_teams ? 8 : 1);
   return f;
 }
 
@@ -903,6 +932,8 @@ static cudaError_t launch_paged_rows_t(PagedAttendArgs a, const PagedRowsShape& 
   a.cut = f.cut;
   a.teams = f.warp_teams ? grid * NW : grid;
   a.run_step = f.warp_teams ? 1 : NW;
+  a.unit_rows = kPR;
+  a.unit_shift = 4;
   cudaError_t e;
   if constexpr (D <= 256) {
     if (f.warp_teams) {
@@ -919,9 +950,7 @@ static cudaError_t launch_paged_rows_t(PagedAttendArgs a, const PagedRowsShape& 
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || !f.cut) return e;
-  const long long warps = (long long)a.total_q * a.hq * ((D + 127) / 128);
-  paged_merge_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_paged_merge(a, stream);
 }
 
 template <int D, bool E4M3>
@@ -932,6 +961,8 @@ static cudaError_t launch_paged_rows_d(const PagedAttendArgs& a, PagedRowsShape 
 
 cudaError_t launch_paged_rows(const PagedAttendArgs& a, const PagedRowsShape& f, bool e4m3, cudaStream_t stream) {
   const long long units = (long long)a.batch * a.row_groups * a.c.hkv;
+  if (units * (((long long)a.max_len + a.max_q) / (f.tile ? 64 : kPB) + 2) > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (f.tile) return launch_paged_tile(a, f, e4m3, stream);
   switch (a.c.d) {
     case 64: return e4m3 ? launch_paged_rows_d<64, true>(a, f, units, stream) : launch_paged_rows_d<64, false>(a, f, units, stream);
     case 128: return e4m3 ? launch_paged_rows_d<128, true>(a, f, units, stream) : launch_paged_rows_d<128, false>(a, f, units, stream);

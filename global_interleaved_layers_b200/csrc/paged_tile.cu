@@ -1,0 +1,1233 @@
+// paged_tile.cu -- decode and verify over a paged KV cache on the tcgen05 tensor cores: up to a
+// few dozen query rows per KV head against a long run of keys.
+//
+// The products are transposed, keys on the MMA's M and rows on N, so that few rows waste
+// nothing but N's granularity of 16:
+//   S^T = K Q^T      M = KT keys (128; 64 for bf16 rows of 512 dims), N, K = head dim
+//   O^T += V^T P^T   M = 128 head dims per block, N, K = KT keys
+// and a page's rows are operands as they lie: K-major for the scores, MN-major for the values.
+// A K=V row is loaded once and serves both ("Visual guide to Gemma 4", section "K=V technique").
+// Its rotated dims (section "p-RoPE"; at most 64 pairs: dims [0, 64) and [d/2, d/2 + 64)) are
+// turned into a side buffer that only the scores read.
+//
+// E4M3 pages are not widened at all: codes go into kind::f8f6f4 MMAs. The other operand is 16-bit
+// information split into two e4m3 columns whose sum it is, x = hi + lo with hi = rn(x) and
+// lo = rn(x - hi): each takes 4 bits, so the pair holds 8, the bits of a bf16 (a bf16 query
+// element is held exactly down to 2^-9; a weight is rounded by at most 2^-8 of itself, as
+// rounding it to bf16 would). N is twice the rows, and with N's granularity of 16 the second
+// half of 8 rows is free. Query rows are scaled by a power of two to a largest magnitude in
+// [128, 256), weights to at most 448. The rotated dims are fp16 (codes turned in fp32, one
+// rounding of 2^-11) in kind::f16 MMAs on the same accumulator. A key's scale multiplies its
+// scores; a value's scale 2^k is folded into its weight: with e = s + k in log2 units, the
+// weight is 2^(e - mv + 7) for a running mv near max e, and the softmax sum takes 2^(s - m) with
+// an m of its own, so scales of any size only move exponents.
+//
+// Work. A unit is up to NR rows of one (sequence, KV head) against all keys its sequence sees.
+// Units go round the CTAs, or the tiles of all units are laid end to end and cut into equal runs,
+// one per CTA (paged_merge_kernel joins the parts). Persistent: barrier phases run on across
+// units, the next unit's query rows are prepared and its first tiles loaded and scored while
+// the last one's products and output finish.
+//
+// Roles (512 threads): warp 0 loads (TMA, one box per page and 128-byte column chunk, a whole
+// tile's boxes back to back so that a row's columns are asked for together); warp 1 owns TMEM
+// and issues the score MMAs, a tile ahead; warp 2 issues the value MMAs; warp 3 clears the rows
+// of a sequence's first and last tile that no query sees (pages may hold anything there, NaN
+// included); the next eight warps (four when the rows take two softmax groups) prepare query
+// rows and turn K=V chunks; the last one or two groups of four warps run the softmax: a thread
+// owns a key (its TMEM lane) and up to 20 rows. The running maxima are only raised when a score
+// passes them by more than the weights' headroom; until then a tile costs each warp one vote and
+// one meeting of four warps, no reduction.
+// Every wait is bounded: one that runs out records a timeout and the CTA unwinds.
+// Bound: HBM, each visible row read once.
+#include <algorithm>
+
+#include "paged.h"
+
+namespace gattn {
+
+namespace {
+
+constexpr int kTThreads = 512;
+constexpr int kTMaxSlots = 28;
+constexpr float kTop8 = 7.f;           // e4m3: the running maximum's weight is 2^7,
+constexpr float kHeadroom8 = 1.75f;    // others up to 2^8.75 < 448
+
+// One unit's run of tiles.
+struct __align__(16) TilePiece {
+  int b, kvh, row0, rows;
+  int tok0, len, first, end;
+  int kt0, ntiles;          // first tile, tiles (0: there are no more pieces)
+  int slot, pad;            // place of a cut unit's part, or -1
+};
+
+template <int SG, int H>
+struct __align__(16) TileHeader {
+  uint64_t full[kTMaxSlots], empty[kTMaxSlots], edge[kTMaxSlots];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t rot_in[4];       // the producer has started the loads of a tile's rotated chunks
+  uint64_t rot_ready[2];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t o_empty, hmeet[2], mma_done[2];
+  uint64_t piece_full[8], piece_empty[8];
+  uint32_t tmem_base;
+  int abort_flag;
+  int viol[2][SG][4];
+  float red[2][SG][2][4][H <= 8 ? 8 : 32];  // [meeting parity][group][maxima or weights' maxima][quadrant][row]
+  float step[SG][2][H];     // a group's factors for sums and output when its references move
+  float refs[2][SG][2][H];  // [unit parity][softmax group]: references of the sums and of the weights
+  float qsc[4][SG * H];         // e4m3: score factor of a unit's rows (unit mod 4)
+  int orow[4][SG * H];          // output row (token x query heads + head) of a unit's rows
+  int qpos[4][SG * H];          // and their positions
+  TilePiece piece[8];
+  double itf[64];           // theta_j / (2 pi), 0 past the rotated pairs
+};
+
+// Shape of a CTA for units of NR = SG * H rows: SG softmax groups, H rows a thread.
+template <int D, bool E4M3, int SG, int H>
+struct TileCfg {
+  static constexpr int KT = (!E4M3 && D == 512) ? 64 : 128;   // keys per tile
+  static constexpr int NR = SG * H;                           // rows of a unit
+  static constexpr int HW = SG == 1 ? 8 : 4;                  // warps for query rows and rotation
+  // columns: the MMA's N, in 16s (8s with 64 keys on M, for the scores: NQ below)
+  static constexpr int N = E4M3 ? (2 * NR + 15) / 16 * 16 : (NR + 15) / 16 * 16;
+  static constexpr int LO = NR;                               // first lo column (e4m3)
+  static constexpr int CH = E4M3 ? D / 128 : D / 64;          // 128-byte chunks of a row
+  static constexpr int PB = D / 128;                          // 128-dim blocks of the output
+  static constexpr int SLOT = KT * 128;
+  static constexpr int NQ = KT == 64 && NR <= 8 ? 8 : N;      // query rows with padding
+  static constexpr int QROT = E4M3 ? 2 * NQ * 128 : 0;        // fp16 rows of the rotated dims
+  static constexpr int QB = CH * NQ * 128 + QROT;
+  static constexpr int P_B = E4M3 ? N * 128 : KT / 64 * N * 128;
+  static constexpr int ROT = 2 * KT * 128;                    // two chunks of 64 dims, 16 bits
+  static constexpr int HEADER = (sizeof(TileHeader<SG, H>) + 1023) / 1024 * 1024;
+  static constexpr int BUDGET = 232448 - 1024 - HEADER;
+  static constexpr int COL_O = 2 * N;
+  static_assert(COL_O + PB * N <= 512, "TMEM columns");
+};
+
+// Frequencies of the first 64 rotary pairs, theta_j / (2 pi), and the factor of 64 pairs on.
+struct TileTurns {
+  double freq[64];
+  double step64;
+};
+
+// Buffers of a launch: two query buffers where they leave at least two tiles of ring.
+struct TileBufs {
+  int nq, nrot, kslots, vslots;  // value ring only for separate values
+};
+template <int D, bool E4M3, int SG, int H>
+__host__ __device__ inline TileBufs tile_bufs(bool kv_same, bool rot) {
+  using C = TileCfg<D, E4M3, SG, H>;
+  // As much ring as three tiles, then a second buffer for the rotated copy, then one for the
+  // next unit's query rows.
+  TileBufs b;
+  const int tile = C::CH * C::SLOT * (kv_same ? 1 : 2);
+  int left = C::BUDGET - C::QB - 2 * C::P_B - (rot ? C::ROT : 0);
+  b.nq = b.nrot = 1;
+  if (!rot) b.nrot = 0;
+  if (rot && left - C::ROT >= 3 * tile) {
+    b.nrot = 2;
+    left -= C::ROT;
+  }
+  if (left - C::QB >= 2 * tile + tile / 2 && (left - C::QB >= 3 * tile || left < 3 * tile)) {
+    b.nq = 2;
+    left -= C::QB;
+  }
+  int slots = left / C::SLOT;
+  if (slots > kTMaxSlots) slots = kTMaxSlots;
+  // the loads run at most four tiles ahead of the rotation (rot_in has four barriers)
+  if (rot && slots > 4 * C::CH) slots = 4 * C::CH;
+  if (kv_same) {
+    b.kslots = slots & ~1;
+    b.vslots = 0;
+  } else {
+    b.kslots = (slots / 2) & ~1;
+    b.vslots = (slots - b.kslots) & ~1;
+  }
+  return b;
+}
+
+// Position in load order to block of 128 dims: the blocks with rotated dims first.
+template <int PB>
+__device__ __forceinline__ int block_at(int i) {
+  if constexpr (PB == 4) return i == 1 ? 2 : i == 2 ? 1 : i;
+  return i;
+}
+// Chunk (128 bytes of a row) at position i of the load order.
+template <int PB, bool E4M3>
+__device__ __forceinline__ int chunk_at(int i) {
+  if constexpr (E4M3) return block_at<PB>(i);
+  return 2 * block_at<PB>(i >> 1) + (i & 1);
+}
+
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// Instruction descriptors: e4m3 operands (format 0), or fp16 ones (format 0 of kind::f16), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_zero_fmt(int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_ld_x4(uint32_t a, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void tmem_ld_x1(uint32_t a, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(a));
+}
+__device__ __forceinline__ void tmem_ld_x8(uint32_t a, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(a));
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t a, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_x4(uint32_t a, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+template <int H>
+__device__ __forceinline__ void tmem_ld_n(uint32_t a, uint32_t* r) {
+  static_assert(H == 8 || H == 20, "rows of a thread");
+  if constexpr (H == 8) {
+    tmem_ld_x8(a, r);
+  } else {
+    tmem_ld_x16(a, r);
+    tmem_ld_x4(a + 16, r + 16);
+  }
+}
+template <int H>
+__device__ __forceinline__ void tmem_st_n(uint32_t a, const uint32_t* r) {
+  if constexpr (H == 8) {
+    tmem_st_x8(a, r);
+  } else {
+    tmem_st_x16(a, r);
+    tmem_st_x4(a + 16, r + 16);
+  }
+}
+
+// A bounded wait. Out of line, as is all that need not be in a role's loop: a CTA runs six
+// different loops, and where their code together does not stay in the SM's instruction caches
+// every tile fetches it again (measured on the 64-key K=V form: 85 KB of code 6,400 cycles a
+// tile, 78 KB 4,050). Each try suspends the warp for a while, so the limit on tries is seconds;
+// running out of them records a timeout.
+__device__ __noinline__ bool thread_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  bool ok = mbar_try_wait(bar, parity);
+#pragma unroll 1
+  for (int n = 0; !ok && !*abort; ++n) {
+    ok = mbar_try_wait(bar, parity);
+    if (n == 1 << 24) {
+      atomicOr(&g_status, kStatusTimeout);
+      *abort = 1;
+    }
+  }
+  return ok;
+}
+// The same by a whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, thread_wait(bar, parity, abort));
+}
+
+__device__ __noinline__ float2 turn_of(double pos, double inv_freq_turns) {
+  float2 r;
+  rope_cos_sin(pos, inv_freq_turns, &r.x, &r.y);
+  return r;
+}
+
+// The CTA's pieces in turn, by one warp: units team, team + teams, ..., or a run of the line of
+// all units' tiles.
+struct TileWalk {
+  int x, x_end, before, b;
+  __device__ __forceinline__ void start(const PagedAttendArgs& a, int lane) {
+    const int team = blockIdx.x;
+    const int total = line_find(a, lane, a.cut ? -1 : team, &b, &before);
+    const int run = run_length(a, total);
+    x = (int)min((long long)team * run, (long long)total);
+    x_end = a.cut ? (int)min((long long)total, (long long)x + run) : total;
+    if (a.cut && x < x_end) line_find(a, lane, x, &b, &before);
+  }
+  __device__ __forceinline__ void next(const PagedAttendArgs& a, int lane, TilePiece& p) {
+    p.ntiles = 0;
+    if (x >= x_end) return;
+    int blocks, units;
+    seq_units(a, b, &blocks, &units);
+    if (x - before >= (a.cut ? blocks * units : units)) {
+      line_find(a, lane, x, &b, &before);
+      seq_units(a, b, &blocks, &units);
+    }
+    const uint32_t in = x - before, per = a.cut ? blocks : 1;
+    const uint32_t u = in / per, lo = in - u * per, hkv = a.c.hkv;
+    const int hi = a.cut ? min(blocks, x_end - x + (int)lo) : blocks;
+    p.slot = lo == 0 && hi == blocks ? -1 : 2 * (int)blockIdx.x + (lo == 0 ? 1 : 0);
+    p.b = b;
+    p.kvh = u % hkv;
+    p.row0 = u / hkv * a.unit_rows;
+    p.tok0 = __ldg(a.cu_q + b);
+    const int n = __ldg(a.cu_q + b + 1) - p.tok0;
+    p.len = __ldg(a.lens + b);
+    p.rows = min(a.unit_rows, n * a.group - p.row0);
+    p.first = keys_first(a, p.len, 0);
+    p.end = p.len + n;
+    p.kt0 = (p.first >> a.unit_shift) + lo;
+    p.ntiles = hi - lo;
+    p.pad = 0;
+    x += a.cut ? p.ntiles : a.teams;
+  }
+};
+
+// Sums over a warp's lanes of 2 CNT values each: at every step a lane hands half of its values
+// to the lane W away and adds the other's; with one value left it adds whole ones.
+template <int W, int CNT>
+__device__ __forceinline__ int scatter_sums(float* x, int lane) {
+  if constexpr (W == 0) {
+    return 0;
+  } else {
+    const bool up = (lane & W) != 0;
+    if constexpr (CNT > 0) {
+#pragma unroll
+      for (int q = 0; q < CNT; ++q) {
+        const float send = up ? x[q] : x[q + CNT], keep = up ? x[q + CNT] : x[q];
+        x[q] = keep + __shfl_xor_sync(0xffffffffu, send, W);
+      }
+    } else {
+      x[0] += __shfl_xor_sync(0xffffffffu, x[0], W);
+    }
+    return (up ? CNT : 0) + scatter_sums<W / 2, CNT / 2>(x, lane);
+  }
+}
+
+__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t x) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(x) : "memory");
+}
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+}  // namespace
+
+template <int D, bool E4M3, bool SAME, int SG, int H>
+__global__ void __launch_bounds__(kTThreads, 1)
+paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                  const __grid_constant__ PagedAttendArgs a, const __grid_constant__ TileTurns turns) {
+  using C = TileCfg<D, E4M3, SG, H>;
+  constexpr int KT = C::KT, N = C::N, NQ = C::NQ, NR = C::NR, CH = C::CH, PB = C::PB, HALF = D / 2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  using Header = TileHeader<SG, H>;
+  Header* hd = reinterpret_cast<Header*>(base);
+  constexpr bool kv_same = SAME;
+  const bool rot = SAME && a.r > 0;
+  const TileBufs bufs = tile_bufs<D, E4M3, SG, H>(kv_same, rot);
+  uint8_t* q_s = base + C::HEADER;
+  uint8_t* p_s = q_s + bufs.nq * C::QB;
+  uint8_t* rot_s = p_s + 2 * C::P_B;
+  uint8_t* kring = rot_s + bufs.nrot * C::ROT;
+  uint8_t* vring = kring + bufs.kslots * C::SLOT;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+#pragma unroll 1
+    for (int s = 0; s < kTMaxSlots; ++s) {
+      mbar_init(&hd->full[s], 1);
+      mbar_init(&hd->empty[s], 1);
+      mbar_init(&hd->edge[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&hd->q_full[i], C::HW);
+      mbar_init(&hd->q_empty[i], 1);
+      mbar_init(&hd->rot_ready[i], C::HW);
+      mbar_init(&hd->s_full[i], 1);
+      mbar_init(&hd->p_full[i], 4 * SG);
+      mbar_init(&hd->pv_done[i], 1);
+      mbar_init(&hd->hmeet[i], 4);
+      mbar_init(&hd->mma_done[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&hd->rot_in[i], 1);
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&hd->piece_full[i], 1);
+      mbar_init(&hd->piece_empty[i], 15);  // every warp but the one that hands pieces out
+    }
+    mbar_init(&hd->o_empty, 4 * SG);
+    hd->abort_flag = 0;
+    fence_barrier_init();
+  }
+  // rows that no unit writes (N's granularity) stay zero in the query and weight buffers
+#pragma unroll 1
+  for (int i = threadIdx.x; i < (bufs.nq * C::QB + 2 * C::P_B) / 16; i += kTThreads)
+    reinterpret_cast<uint4*>(q_s)[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+  for (int j = threadIdx.x; j < 64; j += kTThreads) hd->itf[j] = j < a.r ? turns.freq[j] : 0.0;
+  if (a.chunk_of == nullptr && blockIdx.x == 0)
+#pragma unroll 1
+    for (int b = threadIdx.x; b < a.batch; b += kTThreads) {
+      const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0;
+      if (n != 0 && !seq_ok(a, tok0, n, __ldg(a.lens + b))) atomicOr(&g_status, kStatusSeqlen);
+    }
+  fence_proxy_async_smem();
+  if (warp == 1) {
+    tmem_alloc(&hd->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = hd->tmem_base;
+  volatile int* abort_flag = &hd->abort_flag;
+  TilePiece p;
+  // Piece i of this CTA; false at the end (or on abort).
+  auto piece_at = [&](int i, TilePiece& out) -> bool {
+    if (!warp_wait(&hd->piece_full[i & 7], (uint32_t)(i >> 3) & 1u, abort_flag)) return false;
+    out = hd->piece[i & 7];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&hd->piece_empty[i & 7]);
+    return out.ntiles > 0;
+  };
+  // The same for a role of one thread (warps 0 to 2).
+  auto piece_next = [&](int i, TilePiece& out) -> bool {
+    if (!thread_wait(&hd->piece_full[i & 7], (uint32_t)(i >> 3) & 1u, abort_flag)) return false;
+    out = hd->piece[i & 7];
+    mbar_arrive(&hd->piece_empty[i & 7]);
+    return out.ntiles > 0;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    if (elect_one()) {
+      const int ps = 1 << a.c.page_shift, box = min(ps, KT), boxes = KT / box;
+      int ks = 0, vs = 0, t = 0;
+      uint32_t kph = 0, vph = 0, edge_ph = 0;    // edge_ph bit s: parity of slot s's next edge load
+      uint32_t last_full = 0, last_edge = 0;     // slots whose last load completes on full / edge
+      bool ok = true;
+#pragma unroll 1
+      for (int piece = 0; ok && piece_next(piece, p); ++piece) {
+        const int32_t* table = a.c.table + (size_t)p.b * a.c.max_blocks;
+        // Table entries of a tile's boxes, read a tile ahead; -1 for a box that no query sees
+        int next[8];
+        auto read_entries = [&](int kt) {
+#pragma unroll
+          for (int i = 0; i < KT / 16; ++i) {
+            const int pos = kt * KT + i * box;
+            next[i] = i < boxes && pos < p.end && pos + box > p.first ? __ldg(table + (pos >> a.c.page_shift)) : -1;
+          }
+        };
+        read_entries(p.kt0);
+#pragma unroll 1
+        for (int lt = 0; lt < p.ntiles && ok; ++lt, ++t) {
+          const int kt = p.kt0 + lt, slot_row = (kt * KT) & (ps - 1);  // a box's rows follow the tile's first
+          int plane[8];
+          uint32_t count = 0;
+#pragma unroll
+          for (int i = 0; i < KT / 16; ++i) {
+            const int pos = kt * KT + i * box, e = next[i];
+            const bool used = i < boxes && pos < p.end && pos + box > p.first;
+            plane[i] = used ? e * a.c.hkv + p.kvh : -1;
+            if (used && (unsigned)e >= (unsigned)a.c.num_pages) {
+              atomicOr(&g_status, kStatusPage);
+              plane[i] = a.c.num_pages * a.c.hkv;  // past the pool: zeros
+            }
+            count += used;
+          }
+          if (lt + 1 < p.ntiles) read_entries(kt + 1);
+          const bool cut = kt * KT < p.first || (kt + 1) * KT > p.end;
+          // The tile's chunks, a block's (or two blocks') at a time: its slots are free first, then
+          // its boxes go out together, a row's columns one after the other.
+#pragma unroll 1
+          for (int v = 0; v < (SAME ? 1 : 2) && ok; ++v) {
+            const CUtensorMap* map = v ? &v_map : &k_map;
+            uint8_t* ring = v ? vring : kring;
+            const int bar0 = v ? bufs.kslots : 0, slots = v ? bufs.vslots : bufs.kslots;
+            const bool clear = cut && (SAME || v);
+            int s = v ? vs : ks;
+            uint32_t f = v ? vph : kph;
+            uint64_t* bars = clear ? hd->edge : hd->full;
+            constexpr int G = CH >= 2 ? 2 : 1;  // chunks of a step: slot counts are even, a step does not wrap
+#pragma unroll 1
+            for (int c0 = 0; c0 < CH && ok; c0 += G) {
+#pragma unroll
+              for (int j = 0; j < G; ++j) {
+                ok = ok && thread_wait(&hd->empty[bar0 + s + j], f ^ 1u, abort_flag);
+                const uint32_t bit = 1u << (bar0 + s + j);
+                last_edge = clear ? last_edge | bit : last_edge & ~bit;
+                last_full = clear ? last_full & ~bit : last_full | bit;
+                if (clear) edge_ph ^= bit;
+                if (ok) mbar_arrive_expect_tx(&bars[bar0 + s + j], count * box * 128);
+              }
+              if (!ok) break;
+#pragma unroll
+              for (int i = 0; i < KT / 16; ++i) {
+                if (plane[i] < 0) continue;
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+                  tma_load_3d(ring + (s + j) * C::SLOT + i * box * 128, map, &bars[bar0 + s + j],
+                              chunk_at<PB, E4M3>(c0 + j) * (E4M3 ? 128 : 64), boxes > 1 ? 0 : slot_row, plane[i]);
+              }
+              if (rot && c0 <= (E4M3 ? 1 : 2) && c0 + G > (E4M3 ? (PB > 1 ? 1 : 0) : (PB > 1 ? 2 : 1)))
+                mbar_arrive(&hd->rot_in[t & 3]);  // the rotated chunks' loads have begun: their slots' barriers are in the phase to wait for
+              s += G;
+              if (s == slots) { s = 0; f ^= 1u; }
+            }
+            if (!ok) break;
+            if (v) {
+              vs = s;
+              vph = f;
+            } else {
+              ks = s;
+              kph = f;
+            }
+          }
+        }
+      }
+      // the last load of every slot lands before the CTA can leave (the barrier's phase parity: of a
+      // plain load the one its slot's next fill would flip, of an edge load the last used)
+#pragma unroll 1
+      for (int s = 0; s < bufs.kslots + bufs.vslots; ++s) {
+        if (!(((last_full | last_edge) >> s) & 1u)) continue;
+        const bool on_edge = (last_edge >> s) & 1u;
+        const bool k = s < bufs.kslots;
+        const int nxt = k ? ks : bufs.kslots + vs;
+        const uint32_t ph = k ? kph : vph;
+        const uint32_t par = on_edge ? ((edge_ph >> s) & 1u) ^ 1u : (s < nxt ? ph : ph ^ 1u);
+        const unsigned long long w0 = globaltimer_ns();
+        while (!mbar_try_wait(on_edge ? &hd->edge[s] : &hd->full[s], par) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ score MMAs
+    if (elect_one()) {
+      const uint32_t id16 = E4M3 ? idesc_zero_fmt(KT, NQ, 0, 0) : umma_idesc_bf16(KT, NQ, 0, 0);
+      const uint32_t id8 = idesc_zero_fmt(KT, NQ, 0, 0);
+      int ks = 0, t = 0;
+      uint32_t kph = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int piece = 0; ok && piece_next(piece, p); ++piece) {
+        const int qb = piece % bufs.nq;
+        ok = thread_wait(&hd->q_full[qb], (uint32_t)(piece / bufs.nq) & 1u, abort_flag);
+        const uint64_t q_desc = sdesc_sw128(smem_u32(q_s + qb * C::QB), 16, 1024);
+#pragma unroll 1
+        for (int lt = 0; lt < p.ntiles && ok; ++lt, ++t) {
+          const uint32_t sb = tmem + (uint32_t)(t & 1) * N;
+          // S^T(t) overwrites the scores that softmax(t - 2) read
+          if (t >= 2) ok = thread_wait(&hd->p_full[t & 1], (uint32_t)((t - 2) >> 1) & 1u, abort_flag);
+          uint32_t acc = 0;
+          // first the chunks (their unrotated steps) as they land, two at a time so that the MMAs'
+          // operands are formed ahead of their issue; then the rotated copy
+          constexpr int G = CH >= 2 ? 2 : 1;
+#pragma unroll 1
+          for (int i = 0; i < CH && ok; i += G) {
+#pragma unroll
+            for (int j = 0; j < G; ++j) ok = ok && thread_wait(&hd->full[ks + j], kph, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kd0 = sdesc_sw128(smem_u32(kring + ks * C::SLOT), 16, 1024);
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+              const int c = chunk_at<PB, E4M3>(i + j);
+              const uint64_t kd = kd0 + j * (C::SLOT >> 4);
+              const uint64_t qd = q_desc + (uint64_t)(c * (NQ * 8));
+              if constexpr (E4M3) {
+                // the rotated dims are the first 64 of the row and of its second half
+                const bool first = rot && (c * 128 == 0 || c * 128 == HALF), second = rot && HALF == 64;
+                if (!first) {
+                  umma_f8(sb, kd, qd, id8, acc);
+                  umma_f8(sb, kd + 2, qd + 2, id8, 1);
+                  acc = 1;
+                }
+                if (!second) {
+                  umma_f8(sb, kd + 4, qd + 4, id8, acc);
+                  umma_f8(sb, kd + 6, qd + 6, id8, 1);
+                  acc = 1;
+                }
+              } else if (!(rot && (c == 0 || c == HALF / 64))) {
+                umma_ss(sb, kd, qd, id16, acc);
+                umma_ss(sb, kd + 2, qd + 2, id16, 1);
+                umma_ss(sb, kd + 4, qd + 4, id16, 1);
+                umma_ss(sb, kd + 6, qd + 6, id16, 1);
+                acc = 1;
+              }
+              if (!SAME) umma_commit(&hd->empty[ks + j]);
+            }
+            ks += G;
+            if (ks == bufs.kslots) { ks = 0; kph ^= 1u; }
+          }
+          if (ok && rot) {
+            ok = thread_wait(&hd->rot_ready[t % bufs.nrot], (uint32_t)(t / bufs.nrot) & 1u, abort_flag);
+            tc_fence_after();
+            const uint64_t rd = sdesc_sw128(smem_u32(rot_s + (t % bufs.nrot) * C::ROT), 16, 1024);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (!ok) break;
+              const uint64_t kd = rd + i * (C::SLOT >> 4), qd = q_desc + (uint64_t)((E4M3 ? CH + i : i * (HALF / 64)) * (NQ * 8));
+              umma_ss(sb, kd, qd, id16, acc);
+              umma_ss(sb, kd + 2, qd + 2, id16, 1);
+              umma_ss(sb, kd + 4, qd + 4, id16, 1);
+              umma_ss(sb, kd + 6, qd + 6, id16, 1);
+              acc = 1;
+            }
+          }
+          if (!ok) break;
+          umma_commit(&hd->s_full[t & 1]);
+          if (lt == p.ntiles - 1) umma_commit(&hd->q_empty[qb]);
+        }
+      }
+      umma_commit(&hd->mma_done[0]);
+      const unsigned long long w0 = globaltimer_ns();
+      while (!mbar_try_wait(&hd->mma_done[0], 0) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ value MMAs
+    if (elect_one()) {
+      const uint32_t id = E4M3 ? idesc_zero_fmt(128, N, 1, 0) : umma_idesc_bf16(128, N, 1, 0);
+      const int slots = SAME ? bufs.kslots : bufs.vslots, bar0 = SAME ? 0 : bufs.kslots;
+      uint8_t* ring = SAME ? kring : vring;
+      int vs = 0, t = 0;
+      uint32_t vph = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int piece = 0; ok && piece_next(piece, p); ++piece) {
+#pragma unroll 1
+        for (int lt = 0; lt < p.ntiles && ok; ++lt, ++t) {
+          ok = thread_wait(&hd->p_full[t & 1], (uint32_t)(t >> 1) & 1u, abort_flag);
+          // a unit's first products overwrite the output that the last unit's epilogue has read
+          if (ok && lt == 0 && piece > 0) ok = thread_wait(&hd->o_empty, (uint32_t)(piece - 1) & 1u, abort_flag);
+          const uint32_t p_addr = smem_u32(p_s + (t & 1) * C::P_B);
+#pragma unroll 1
+          for (int i = 0; i < PB && ok; ++i) {
+            constexpr int per = CH / PB;  // chunks of a block
+            if (!SAME)                    // K=V chunks have landed: the scores of this tile needed them
+#pragma unroll
+              for (int j = 0; j < per; ++j) ok = ok && thread_wait(&hd->full[bar0 + vs + j], vph, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = sdesc_sw128(smem_u32(ring + vs * C::SLOT), C::SLOT, 1024);
+            const uint64_t pd = sdesc_sw128(p_addr, 16, 1024);
+            const uint32_t d = tmem + C::COL_O + (uint32_t)block_at<PB>(i) * N;
+#pragma unroll
+            for (int kk = 0; kk < KT / (E4M3 ? 32 : 16); ++kk) {
+              const uint32_t acc = kk != 0 ? 1u : (uint32_t)(lt != 0);
+              if constexpr (E4M3) umma_f8(d, vd + 256 * kk, pd + 2 * kk, id, acc);
+              else umma_ss(d, vd + 128 * kk, pd + (kk >> 2) * (N * 8) + 2 * (kk & 3), id, acc);
+            }
+#pragma unroll
+            for (int j = 0; j < per; ++j) umma_commit(&hd->empty[bar0 + vs + j]);
+            vs += per;
+            if (vs == slots) { vs = 0; vph ^= 1u; }
+          }
+          if (!ok) break;
+          umma_commit(&hd->pv_done[t & 1]);
+        }
+      }
+      umma_commit(&hd->mma_done[1]);
+      const unsigned long long w0 = globaltimer_ns();
+      while (!mbar_try_wait(&hd->mma_done[1], 0) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ pieces, clearing of cut tiles
+    TileWalk walk;
+    walk.start(a, lane);
+    int made = 0, last = -100;             // pieces handed out; the index of the end mark
+    auto hand_out = [&]() -> bool {
+      if (last != -100) return true;
+      if (made >= 8 && !warp_wait(&hd->piece_empty[made & 7], (uint32_t)((made >> 3) - 1) & 1u, abort_flag)) return false;
+      walk.next(a, lane, p);
+      if (lane == 0) hd->piece[made & 7] = p;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&hd->piece_full[made & 7]);
+      if (p.ntiles == 0) last = made;
+      ++made;
+      return true;
+    };
+    bool ok = true;
+    const int slots = kv_same ? bufs.kslots : bufs.vslots, bar0 = kv_same ? 0 : bufs.kslots;
+    uint8_t* ring = kv_same ? kring : vring;
+    int s = 0;
+    uint32_t edge_ph = 0;
+#pragma unroll 1
+    for (int piece = -4; ok && piece != last; ++piece) {  // pieces are handed out four ahead
+      ok = hand_out();
+      __syncwarp();
+      if (piece < 0) continue;
+      p = hd->piece[piece & 7];            // handed out four pieces ago: not replaced before eight
+#pragma unroll 1
+      for (int lt = 0; lt < p.ntiles && ok; ++lt) {
+        const int k0 = (p.kt0 + lt) * KT;
+        const int lo = max(p.first - k0, 0), hi = min(p.end - k0, KT);
+#pragma unroll 1
+        for (int i = 0; i < CH && ok; ++i) {
+          if (lo > 0 || hi < KT) {
+            ok = warp_wait(&hd->edge[bar0 + s], (edge_ph >> s) & 1u, abort_flag);
+            if (!ok) break;
+            edge_ph ^= 1u << s;
+            uint4* rows = reinterpret_cast<uint4*>(ring + s * C::SLOT);
+#pragma unroll 1
+            for (int x = lane; x < lo * 8; x += 32) rows[x] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+            for (int x = hi * 8 + lane; x < KT * 8; x += 32) rows[x] = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&hd->full[bar0 + s]);
+          }
+          if (++s == slots) s = 0;
+        }
+      }
+    }
+  } else if (warp < 4 + C::HW) {
+    // ------------------------------------------------------------ query rows, rotation of K=V chunks
+    const int hw = warp - 4;
+    const int ht = threadIdx.x - 128;
+    TilePiece np;
+    bool more = piece_at(0, np);
+    int q_piece = 0;
+    auto prepare = [&]() -> bool {         // query rows of piece np, when there is one; false on abort
+      if (!more) return true;
+      const int qb = q_piece % bufs.nq;
+      if (q_piece >= bufs.nq &&
+          !warp_wait(&hd->q_empty[qb], (uint32_t)(q_piece / bufs.nq - 1) & 1u, abort_flag))
+        return false;
+      uint8_t* qd = q_s + qb * C::QB;
+      constexpr int QI = (HALF + 63) / 64;   // words of two pairs per lane and half row
+#pragma unroll 1
+      for (int row = hw; row < NR; row += C::HW) {
+        const bool have = row < np.rows;
+        const int tk = (np.row0 + row) / a.group, hh = np.row0 + row - tk * a.group;
+        const int orow = (np.tok0 + tk) * a.hq + np.kvh * a.group + hh;
+        const uint16_t* src = a.q + (size_t)orow * D;
+        if (lane == 0) {
+          hd->orow[q_piece & 3][row] = orow;
+          hd->qpos[q_piece & 3][row] = np.len + tk;
+        }
+        // e4m3 goes over the row twice: for its largest magnitude, then to scale and split it
+        uint32_t top = 0;
+        float up = 1.f;
+#pragma unroll 1
+        for (int i = 0; i < (E4M3 ? 2 : 1) * QI; ++i) {
+          const bool store = !E4M3 || i >= QI;
+          if (E4M3 && i == QI) {
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+            // the largest magnitude is in [2^(E - 127), 2^(E - 126)): to [2^7, 2^8) by 2^(134 - E). A
+            // NaN or an infinity must reach the row's scores, and goes into the row's factor.
+            const int E = (int)(top >> 23);
+            const int k = top == 0u || E == 255 ? 0 : min(max(134 - E, -126), 126);
+            up = __uint_as_float((uint32_t)(127 + k) << 23);
+            if (lane == 0)
+              hd->qsc[q_piece & 3][row] =
+                  E == 255 ? __uint_as_float(0x7FC00000u)
+                           : a.softmax_scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 - k) << 23);
+          }
+          const int far = i % QI, j = 2 * lane + 64 * far;
+          if (j >= HALF) continue;
+          uint32_t w0 = 0u, w1 = 0u;
+          if (have) {
+            w0 = __ldg(reinterpret_cast<const uint32_t*>(src + j));
+            w1 = __ldg(reinterpret_cast<const uint32_t*>(src + HALF + j));
+          }
+          float x00 = __uint_as_float(w0 << 16), x01 = __uint_as_float(w0 & 0xFFFF0000u);
+          float x10 = __uint_as_float(w1 << 16), x11 = __uint_as_float(w1 & 0xFFFF0000u);
+          if (j < a.r) {
+            double f0 = turns.freq[2 * lane], f1 = turns.freq[2 * lane + 1];  // `far` times 64 pairs on
+#pragma unroll 1
+            for (int k = 0; k < far; ++k) {
+              f0 *= turns.step64;
+              f1 *= turns.step64;
+            }
+            const float2 c0 = turn_of((double)(np.len + tk), f0), c1 = turn_of((double)(np.len + tk), j + 1 < a.r ? f1 : 0.0);
+            w0 = pack_bf16x2(x00 * c0.x - x10 * c0.y, x01 * c1.x - x11 * c1.y);
+            w1 = pack_bf16x2(x00 * c0.y + x10 * c0.x, x01 * c1.y + x11 * c1.x);
+          }
+          if (!store) {
+            top = max(max(top, max((w0 & 0x7FFFu) << 16, w0 & 0x7FFF0000u)), max((w1 & 0x7FFFu) << 16, w1 & 0x7FFF0000u));
+            continue;
+          }
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {
+            const int dim = part * HALF + j;
+            const uint32_t w = part ? w1 : w0;
+            if constexpr (!E4M3) {
+              *reinterpret_cast<uint32_t*>(qd + (dim >> 6) * NQ * 128 + sw128(row, (dim & 63) * 2)) = w;
+            } else {
+              const float x0 = __uint_as_float(w << 16) * up, x1 = __uint_as_float(w & 0xFFFF0000u) * up;
+              const uint32_t hi = e4m3x2(x0, x1);
+              const float2 h = unpack_f16x2(e4m3_lo(hi));
+              uint8_t* chunk = qd + (dim >> 7) * NQ * 128;
+              *reinterpret_cast<uint16_t*>(chunk + sw128(row, dim & 127)) = (uint16_t)hi;
+              *reinterpret_cast<uint16_t*>(chunk + sw128(C::LO + row, dim & 127)) = (uint16_t)e4m3x2(x0 - h.x, x1 - h.y);
+              if (j < 64) *reinterpret_cast<uint32_t*>(qd + (CH + part) * NQ * 128 + sw128(row, j * 2)) = pack_f16x2(x0, x1);
+            }
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&hd->q_full[qb]);
+      ++q_piece;
+      return true;
+    };
+    bool ok = prepare();
+    int t = 0, ks = 0;
+    uint32_t kph = 0;
+    // Rotation: thread (unit ku of 4 pairs, key group kg): keys kg, kg + KG, ... of the tile.
+    constexpr int KG = C::HW * 2;          // 16 or 8 groups of keys
+    const int ku = ht & 15, kg = ht >> 4;
+    float sc[4], ss[4], tc[4], ts[4];      // turns of KG keys and of a tile
+    if (rot) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 one = turn_of((double)KG, hd->itf[4 * ku + e]), all = turn_of((double)KT, hd->itf[4 * ku + e]);
+        sc[e] = one.x;
+        ss[e] = one.y;
+        tc[e] = all.x;
+        ts[e] = all.y;
+      }
+    }
+#pragma unroll 1
+    for (int piece = 0; ok && more; ++piece) {
+      // with two query buffers the next unit's rows are made ahead of this one's tiles; with one
+      // they wait for this unit's last scores
+      p = np;
+      more = piece_at(piece + 1, np);
+      if (bufs.nq == 2) ok = prepare();
+      if (rot) {
+        float ac[4], as[4];
+#pragma unroll 1
+        for (int lt = 0; lt < p.ntiles && ok; ++lt, ++t) {
+          const int key0 = (p.kt0 + lt) * KT + kg;
+          if ((lt & 15) == 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 cs = turn_of((double)key0, hd->itf[4 * ku + e]);
+              ac[e] = cs.x;
+              as[e] = cs.y;
+            }
+          }
+          // the slots of the two rotated chunks, whose loads have begun (so that their barriers'
+          // phases are the ones to wait for), and the copy's buffer, whose last scores are done
+          const int i1 = E4M3 ? (PB > 1 ? 1 : 0) : (PB > 1 ? 2 : 1);
+          int s1 = ks + i1;
+          const bool wrap = s1 >= bufs.kslots;
+          if (wrap) s1 -= bufs.kslots;
+          ok = warp_wait(&hd->rot_in[t & 3], (uint32_t)(t >> 2) & 1u, abort_flag);
+          if (ok && t >= bufs.nrot)
+            ok = warp_wait(&hd->s_full[(t - bufs.nrot) & 1], (uint32_t)((t - bufs.nrot) >> 1) & 1u, abort_flag);
+          if (ok) ok = warp_wait(&hd->full[ks], kph, abort_flag);
+          if (ok) ok = warp_wait(&hd->full[s1], wrap ? kph ^ 1u : kph, abort_flag);
+          if (!ok) break;
+          const uint8_t* c0 = kring + ks * C::SLOT;
+          const uint8_t* c1 = kring + s1 * C::SLOT;
+          uint8_t* dst = rot_s + (t % bufs.nrot) * C::ROT;
+          float bc[4], bs[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            bc[e] = ac[e];
+            bs[e] = as[e];
+          }
+#pragma unroll 4
+          for (int key = 0; key < KT / KG; ++key) {
+            const int row = kg + KG * key;
+            float x0[4], x1[4], y0[4], y1[4];
+            if constexpr (E4M3) {
+              // dims 4 ku .. in the first chunk's first 64 columns; the partners in the second
+              // chunk's, or (128 dims) the first chunk's last 64
+              e4m3x4_to_f32(*reinterpret_cast<const uint32_t*>(c0 + sw128(row, 4 * ku)), x0);
+              e4m3x4_to_f32(*reinterpret_cast<const uint32_t*>(c1 + sw128(row, (PB > 1 ? 0 : 64) + 4 * ku)), x1);
+            } else {
+              const uint2 u0 = *reinterpret_cast<const uint2*>(c0 + sw128(row, 8 * ku));
+              const uint2 u1 = *reinterpret_cast<const uint2*>(c1 + sw128(row, 8 * ku));
+              x0[0] = __uint_as_float(u0.x << 16); x0[1] = __uint_as_float(u0.x & 0xFFFF0000u);
+              x0[2] = __uint_as_float(u0.y << 16); x0[3] = __uint_as_float(u0.y & 0xFFFF0000u);
+              x1[0] = __uint_as_float(u1.x << 16); x1[1] = __uint_as_float(u1.x & 0xFFFF0000u);
+              x1[2] = __uint_as_float(u1.y << 16); x1[3] = __uint_as_float(u1.y & 0xFFFF0000u);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y0[e] = x0[e] * bc[e] - x1[e] * bs[e];
+              y1[e] = x0[e] * bs[e] + x1[e] * bc[e];
+              const float nc = bc[e] * sc[e] - bs[e] * ss[e];
+              bs[e] = bc[e] * ss[e] + bs[e] * sc[e];
+              bc[e] = nc;
+            }
+            const uint32_t off = sw128(row, 8 * ku);
+            *reinterpret_cast<uint2*>(dst + off) =
+                E4M3 ? make_uint2(pack_f16x2(y0[0], y0[1]), pack_f16x2(y0[2], y0[3])) : make_uint2(pack_bf16x2(y0[0], y0[1]), pack_bf16x2(y0[2], y0[3]));
+            *reinterpret_cast<uint2*>(dst + C::SLOT + off) =
+                E4M3 ? make_uint2(pack_f16x2(y1[0], y1[1]), pack_f16x2(y1[2], y1[3])) : make_uint2(pack_bf16x2(y1[0], y1[1]), pack_bf16x2(y1[2], y1[3]));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&hd->rot_ready[t % bufs.nrot]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // the next tile's first angle
+            const float nc = ac[e] * tc[e] - as[e] * ts[e];
+            as[e] = ac[e] * ts[e] + as[e] * tc[e];
+            ac[e] = nc;
+          }
+          ks += CH;
+          if (ks >= bufs.kslots) { ks -= bufs.kslots; kph ^= 1u; }
+        }
+      }
+      if (ok && bufs.nq == 1) ok = prepare();
+    }
+  } else {
+    // ------------------------------------------------------------ softmax and output
+    const int quad = warp & 3, half = (warp - 4 - C::HW) >> 2;
+    const uint32_t lane_tmem = tmem + ((uint32_t)(quad * 32) << 16) + half * H;
+    const bool key_lane = KT == 128 || lane < 16;             // TMEM lanes of M = 64: 16 per quadrant
+    const int u = KT == 128 ? quad * 32 + lane : quad * 16 + (lane & 15);
+    // Headroom over the running references: weights of up to 2^8, in e4m3 up to 2^8.75 < 448 (its
+    // reference is kept kTop8 = 7 below the maximum, so that the largest weight is 2^7).
+    constexpr float kRoom = 8.f, kRoom8 = kTop8 + kHeadroom8;
+    // Where this thread's weights go: byte column of its key, swizzled, by row mod 8
+    uint32_t col[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int cb = E4M3 ? u : (u & 63) * 2, r7 = (j + half * H) & 7;
+      col[j] = (((cb >> 4) ^ r7) << 4) | (cb & 15);
+    }
+    const uint32_t p_mine = smem_u32(p_s) + half * H * 128 + (E4M3 ? 0 : (u >> 6) * N * 128);
+    uint32_t meets = 0;
+    bool ok = true;
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&hd->hmeet[half]);
+      ok = warp_wait(&hd->hmeet[half], meets & 1u, abort_flag);
+      ++meets;
+    };
+    int t = 0;
+#pragma unroll 1
+    for (int piece = 0; ok && piece_at(piece, p); ++piece) {
+      // m: reference of the sums; mv: of the weights (bf16: the same one). A row that has seen no key
+      // has the lowest finite number.
+      float m_run[H], mv_run[E4M3 ? H : 1], l_acc[H];
+#pragma unroll
+      for (int q = 0; q < H; ++q) {
+        m_run[q] = -3.3e38f;
+        if constexpr (E4M3) mv_run[q] = -3.3e38f;
+        l_acc[q] = 0.f;
+      }
+      // the references are the same in every lane and warp of the group; a copy in shared memory
+      // serves what runs once in a while (the group meets before anyone reads it)
+      if (quad == 0 && lane < H) hd->refs[piece & 1][half][0][lane] = hd->refs[piece & 1][half][1][lane] = -3.3e38f;
+      // e4m3: this thread's key's scales are read a tile ahead, the table entry that leads to
+      // them two tiles ahead, so that no tile waits for either
+      float ks_next = 1.f, vs_next = 1.f;
+      int entry = -1;
+      auto read_ahead = [&](int lt) {  // scales of tile lt, entry of tile lt + 1
+        const int pos = (p.kt0 + lt) * KT + u, ps = a.c.page_shift;
+        ks_next = vs_next = 1.f;
+        if ((unsigned)entry < (unsigned)a.c.num_pages) {
+          const size_t row = page_row(a.c, entry, p.kvh, pos & ((1 << ps) - 1));
+          ks_next = __ldg(a.c.k_scales + row);
+          if (!SAME) vs_next = __ldg(a.c.v_scales + row);
+        }
+        const int np = pos + KT;
+        entry = lt + 1 < p.ntiles && np >= p.first && np < p.end ? __ldg(a.c.table + (size_t)p.b * a.c.max_blocks + (np >> ps)) : -1;
+      };
+#pragma unroll 1
+      for (int lt = E4M3 ? -2 : 0; lt < p.ntiles && ok; ++lt) {
+        float kscale = 1.f, vscale = 1.f;
+        if constexpr (E4M3) {
+          kscale = ks_next;
+          vscale = SAME ? ks_next : vs_next;
+          read_ahead(lt + 1);
+          if (lt < 0) continue;
+        }
+        const int bb = t & 1, k0 = (p.kt0 + lt) * KT;
+        ok = warp_wait(&hd->s_full[bb], (uint32_t)(t >> 1) & 1u, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        // sv: scores in log2 units; lv: log2 of the value scale, a power of two (NaN stays NaN)
+        float sv[H], lv = 0.f;
+        tmem_ld_n<H>(lane_tmem + bb * N, reinterpret_cast<uint32_t*>(sv));
+        if constexpr (E4M3) {
+          lv = vscale == vscale ? (float)((int)(__float_as_uint(vscale) >> 23) - 127) : vscale;
+          float s2[H];
+          tmem_ld_n<H>(lane_tmem + bb * N + C::LO, reinterpret_cast<uint32_t*>(s2));
+          tmem_ld_wait();
+          const float* cf = &hd->qsc[piece & 3][half * H];
+#pragma unroll
+          for (int q = 0; q < H; ++q) sv[q] = (sv[q] + s2[q]) * (cf[q] * kscale);
+        } else {
+          tmem_ld_wait();
+          const float cf = a.softmax_scale * 1.4426950408889634f;
+#pragma unroll
+          for (int q = 0; q < H; ++q) sv[q] *= cf;
+        }
+        // tiles that every row sees whole need no mask (rows past the unit's read zero queries)
+        if (k0 + KT - 1 > p.len || k0 < p.first || (a.is_local && k0 < p.end - a.window) || !key_lane) {
+          const int pos = key_lane ? k0 + u : 0x7fffffff;
+#pragma unroll
+          for (int q = 0; q < H; ++q) {
+            const int qp = hd->qpos[piece & 3][half * H + q];
+            if (pos > qp || (a.is_local && pos <= qp - a.window)) sv[q] = -INFINITY;
+          }
+        }
+        // ---- does any score pass its reference by more than the headroom?
+        float over = -INFINITY, over8 = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < H; ++q) {
+          over = fmaxf(over, sv[q] - m_run[q]);
+          if constexpr (E4M3) over8 = fmaxf(over8, sv[q] - mv_run[q]);
+        }
+        bool pass = over > kRoom || (E4M3 && over8 + lv > kRoom8);
+        pass = __any_sync(0xffffffffu, pass);
+        if (lane == 0) hd->viol[meets & 1u][half][quad] = pass;
+        meet();
+        if (!ok) break;
+        const int4 vv = *reinterpret_cast<const int4*>(hd->viol[(meets - 1) & 1u][half]);
+        if (vv.x | vv.y | vv.z | vv.w) {
+          // the four warps agree on the tile's maxima and raise the references to them
+          auto& red = hd->red[meets & 1u][half];
+          {
+            float y[H], z[H];
+#pragma unroll
+            for (int q = 0; q < H; ++q) {
+              y[q] = warp_max(sv[q]);
+              z[q] = E4M3 ? warp_max(sv[q] + lv) : 0.f;
+            }
+            if (lane == 0) {
+#pragma unroll
+              for (int q = 0; q < H; q += 4) {
+                *reinterpret_cast<float4*>(&red[0][quad][q]) = make_float4(y[q], y[q + 1], y[q + 2], y[q + 3]);
+                if (E4M3) *reinterpret_cast<float4*>(&red[1][quad][q]) = make_float4(z[q], z[q + 1], z[q + 2], z[q + 3]);
+              }
+            }
+          }
+          meet();
+          if (!ok) break;
+          // one warp forms the new references and the factors, the others take them from it
+          auto& refs = hd->refs[piece & 1][half];
+          if (quad == 0 && lane < H) {
+            auto top4 = [&](const float(*x)[H <= 8 ? 8 : 32]) { return fmaxf(fmaxf(x[0][lane], x[1][lane]), fmaxf(x[2][lane], x[3][lane])); };
+            const float m_old = refs[0][lane], m_new = fmaxf(m_old, top4(red[0]));
+            float f = fast_exp2(m_old - m_new);
+            refs[0][lane] = m_new;
+            hd->step[half][0][lane] = f;
+            if constexpr (E4M3) {
+              const float mv_old = refs[1][lane], mv_new = fmaxf(mv_old, top4(red[1]) - kTop8);
+              refs[1][lane] = mv_new;
+              f = fast_exp2(mv_old - mv_new);
+            }
+            hd->step[half][1][lane] = f;
+          }
+          meet();
+          if (!ok) break;
+          float al[H];
+#pragma unroll
+          for (int q = 0; q < H; ++q) {
+            m_run[q] = refs[0][q];
+            if constexpr (E4M3) mv_run[q] = refs[1][q];
+            l_acc[q] *= hd->step[half][0][q];
+            al[q] = hd->step[half][1][q];
+          }
+          // O^T is touched once the products of the tile before are done (a unit's first tile has
+          // nothing to rescale)
+          if (lt >= 1) {
+            ok = warp_wait(&hd->pv_done[bb ^ 1], (uint32_t)((t - 1) >> 1) & 1u, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          if (lt >= 1) {
+#pragma unroll 1
+            for (int i = 0; i < PB * (E4M3 ? 2 : 1); ++i) {
+              uint32_t o[H];
+              const uint32_t ta = lane_tmem + C::COL_O + (uint32_t)((i % PB) * N + (i / PB) * C::LO);
+              tmem_ld_n<H>(ta, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int q = 0; q < H; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * al[q]);
+              tmem_st_n<H>(ta, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        // ---- weights: buffer bb was read by the products of tile t - 2
+        if (t >= 2) {
+          ok = warp_wait(&hd->pv_done[bb], (uint32_t)((t - 2) >> 1) & 1u, abort_flag);
+          if (!ok) break;
+        }
+        const uint32_t pb = p_mine + bb * C::P_B;
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int q = 0; q < H; q += 2) {
+            l_acc[q] += fast_exp2(sv[q] - m_run[q]);
+            l_acc[q + 1] += fast_exp2(sv[q + 1] - m_run[q + 1]);
+            const float w0 = fast_exp2(sv[q] + lv - mv_run[q]), w1 = fast_exp2(sv[q + 1] + lv - mv_run[q + 1]);
+            const uint32_t hi = e4m3x2(w0, w1);
+            const float2 h = unpack_f16x2(e4m3_lo(hi));
+            const uint32_t lo = e4m3x2(w0 - h.x, w1 - h.y);
+            st_shared_u8(pb + q * 128 + col[q & 7], hi);
+            st_shared_u8(pb + (q + 1) * 128 + col[(q + 1) & 7], hi >> 8);
+            // LO is a multiple of 8 rows: the same swizzle
+            st_shared_u8(pb + (C::LO + q) * 128 + col[q & 7], lo);
+            st_shared_u8(pb + (C::LO + q + 1) * 128 + col[(q + 1) & 7], lo >> 8);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < H; ++q) {
+            const __nv_bfloat16 w = __float2bfloat16_rn(fast_exp2(sv[q] - m_run[q]));
+            l_acc[q] += __bfloat162float(w);
+            if (key_lane) st_shared_u16(pb + q * 128 + col[q & 7], __bfloat16_as_ushort(w));
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&hd->p_full[bb]);
+        ++t;
+      }
+      if (!ok) break;
+      // ---- the unit's (or its part's) output. The rows' sums: halves of the values go to the lanes of
+      // either half of the warp until each lane holds one row, then over the four warps.
+      {
+        constexpr int HP = H <= 8 ? 8 : 32;
+        float x[HP];
+#pragma unroll
+        for (int q = 0; q < HP; ++q) x[q] = q < H ? l_acc[q] : 0.f;
+        const int mine = scatter_sums<16, HP / 2>(x, lane);  // the row this lane ends up with
+        auto& red = hd->red[meets & 1u][half];
+        if ((lane & (32 / HP - 1)) == 0) red[0][quad][mine] = x[0];
+        meet();
+        if (!ok) break;
+      }
+      ok = warp_wait(&hd->pv_done[(t - 1) & 1], (uint32_t)((t - 1) >> 1) & 1u, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      // lane q forms row q's factor, log-sum-exp and place
+      float fac_lane = 0.f;
+      int place = -1;
+      if (lane < H && half * H + lane < p.rows) {
+        const auto& red = hd->red[(meets - 1) & 1u][half];
+        const float l = (red[0][0][lane] + red[0][1][lane]) + (red[0][2][lane] + red[0][3][lane]), m = hd->refs[piece & 1][half][0][lane], mv = hd->refs[piece & 1][half][1][lane];
+        const int row = half * H + lane;
+        place = p.slot >= 0 ? p.slot * NR + row : hd->orow[piece & 3][row];
+        fac_lane = l > 0.f ? __fdividef(1.f, l) : l == 0.f ? 0.f : l;  // a NaN sum stays one
+        if (E4M3) fac_lane *= fast_exp2(fmaxf(mv, -3.0e38f) - fmaxf(m, -3.0e38f));
+        if (quad == 0) {
+          const float lse = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : l == 0.f ? -INFINITY : l;
+          if (p.slot >= 0) a.partial_lse[place] = lse;
+          else if (a.lse) a.lse[place] = lse;
+        }
+      }
+      const bool wide = p.slot >= 0 || a.out_f32;
+      uint8_t* out = p.slot >= 0 ? reinterpret_cast<uint8_t*>(a.partial_o) : static_cast<uint8_t*>(a.out);
+      // a row and a block of 128 dims at a time: 32 dims a warp
+#pragma unroll 1
+      for (int i = 0; i < PB * H; ++i) {
+        const int m = i / H, q = i - m * H, pl = __shfl_sync(0xffffffffu, place, q);
+        if (pl >= 0) {
+          uint32_t o[2];
+          tmem_ld_x1(lane_tmem + C::COL_O + (uint32_t)(m * N + q), o);
+          if constexpr (E4M3) tmem_ld_x1(lane_tmem + C::COL_O + (uint32_t)(m * N + C::LO + q), o + 1);
+          tmem_ld_wait();
+          const float sum = E4M3 ? __uint_as_float(o[0]) + __uint_as_float(o[1]) : __uint_as_float(o[0]);
+          const float v = sum * __shfl_sync(0xffffffffu, fac_lane, q);
+          const size_t at = (size_t)pl * D + m * 128 + quad * 32 + lane;
+          if (wide) reinterpret_cast<float*>(out)[at] = v;
+          else reinterpret_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+        }
+      }
+      // O^T has been read: the next unit's first products may overwrite it
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&hd->o_empty);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// 3-D map over a page pool's byte rows or bf16 rows, 128-byte wide boxes of `rows` rows.
+static bool tile_map(CUtensorMap* m, const void* base, const PagedCache& c, bool e4m3, int rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int esz = e4m3 ? 1 : 2, ps = 1 << c.page_shift;
+  cuuint64_t dims[3] = {(cuuint64_t)c.d, (cuuint64_t)ps, (cuuint64_t)c.num_pages * c.hkv};
+  cuuint64_t strides[2] = {(cuuint64_t)c.d * esz, (cuuint64_t)c.d * ps * esz};
+  cuuint32_t box[3] = {(cuuint32_t)(128 / esz), (cuuint32_t)rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The last table made on this thread is kept: every layer of a kind has the same one.
+static const TileTurns& tile_turns(int d, double log2_base) {
+  static thread_local TileTurns t;
+  static thread_local int last_d = 0;
+  static thread_local double last_base = 0.0;
+  if (last_d != d || last_base != log2_base) {
+    for (int j = 0; j < 64; ++j) t.freq[j] = exp2(-2.0 * j / d * log2_base) * 0.15915494309189533577;
+    t.step64 = exp2(-128.0 / d * log2_base);
+    last_d = d;
+    last_base = log2_base;
+  }
+  return t;
+}
+
+template <int D, bool E4M3, bool SAME, int SG, int H>
+static cudaError_t launch_tile_t(PagedAttendArgs a, bool cut, long long units, cudaStream_t stream) {
+  using C = TileCfg<D, E4M3, SG, H>;
+  const TileBufs b = tile_bufs<D, E4M3, SG, H>(SAME, SAME && a.r > 0);
+  if (b.kslots < C::CH || (!SAME && b.vslots < C::CH)) return cudaErrorInvalidValue;
+  static std::atomic<bool> ready[64];
+  cudaError_t e = allow_smem(paged_tile_kernel<D, E4M3, SAME, SG, H>, 232448, ready);
+  if (e != cudaSuccess) return e;
+  const int box = std::min(1 << a.c.page_shift, C::KT);
+  CUtensorMap k, v;
+  if (!tile_map(&k, a.c.k, a.c, E4M3, box)) return cudaErrorInvalidValue;
+  v = k;
+  if (!SAME && !tile_map(&v, a.c.v, a.c, E4M3, box)) return cudaErrorInvalidValue;
+  const int grid = cut ? kSms : (int)std::min<long long>(units, kSms);
+  a.cut = cut;
+  a.teams = grid;
+  a.run_step = 1;
+  a.unit_rows = C::NR;
+  a.unit_shift = C::KT == 128 ? 7 : 6;
+  paged_tile_kernel<D, E4M3, SAME, SG, H><<<grid, kTThreads, 232448, stream>>>(k, v, a, tile_turns(D, a.log2_base));
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !cut) return e;
+  return launch_paged_merge(a, stream);
+}
+
+template <int D, bool E4M3>
+static cudaError_t launch_tile_d(const PagedAttendArgs& a, const PagedRowsShape& f, long long units, cudaStream_t stream) {
+  const bool same = a.c.v == nullptr;
+  switch (f.unit_rows) {
+    case 8: return same ? launch_tile_t<D, E4M3, true, 1, 8>(a, f.cut, units, stream) : launch_tile_t<D, E4M3, false, 1, 8>(a, f.cut, units, stream);
+    case 40: return same ? launch_tile_t<D, E4M3, true, 2, 20>(a, f.cut, units, stream) : launch_tile_t<D, E4M3, false, 2, 20>(a, f.cut, units, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_paged_tile(const PagedAttendArgs& a, const PagedRowsShape& f, bool e4m3, cudaStream_t stream) {
+  const long long units = (long long)a.batch * a.row_groups * a.c.hkv;
+  switch (a.c.d) {
+    case 128: return e4m3 ? launch_tile_d<128, true>(a, f, units, stream) : launch_tile_d<128, false>(a, f, units, stream);
+    case 256: return e4m3 ? launch_tile_d<256, true>(a, f, units, stream) : launch_tile_d<256, false>(a, f, units, stream);
+    case 512: return e4m3 ? launch_tile_d<512, true>(a, f, units, stream) : launch_tile_d<512, false>(a, f, units, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace gattn
