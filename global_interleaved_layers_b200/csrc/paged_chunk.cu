@@ -257,133 +257,169 @@ __device__ __forceinline__ void turn8(const float* x0, const float* x1, const fl
   }
 }
 
-// 8 elements of a page row, in fp32.
-template <bool E4M3>
-__device__ __forceinline__ void load8(const uint8_t* row, int dim, float scale, float* f) {
-  if constexpr (E4M3) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(row + dim));
-    e4m3x4_to_f32(w.x, f);
-    e4m3x4_to_f32(w.y, f + 4);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] *= scale;
-  } else {
-    bf8_to_f32(__ldg(reinterpret_cast<const uint4*>(row + 2 * dim)), f);
-  }
-}
-
 constexpr int kSideThreads = 256;
-constexpr int kSideRows = 32;  // rows of a block's step: 8 threads a row
+constexpr int kSideHeads = 4;    // heads whose loads are in flight together
+constexpr int kSideQHeads = 8;   // query heads of an item
 
 }  // namespace
 
-// Blocks walk first the query rows (32 tokens a step), then the key rows (a quarter of a tile a
-// step). A thread owns 8 pairs (j, j + d/2) of a row, computes their angles once and goes over
-// the heads.
+// Threads walk items: 8 pairs (j, j + d/2) of one row in a few heads, whose angles are formed
+// once. First the query rows, then the key rows of every tile (those with rotated chunks; with
+// e4m3 all), then, for bf16 pages, the tiles that a sequence's ends cut.
 template <bool E4M3>
 __global__ void __launch_bounds__(kSideThreads) chunk_side_kernel(PagedAttendArgs a, ChunkPlan p) {
+  __shared__ double s_freq[256];
   const int d = a.c.d, half = d / 2, groups = d / 16, hkv = a.c.hkv;
-  const int row = threadIdx.x >> 3, lane8 = threadIdx.x & 7;
-  const int qsteps = p.q_mask ? (a.total_q + kSideRows - 1) / kSideRows : 0;
-  const long long steps = qsteps + (long long)p.tile0[a.batch] * (kCN / kSideRows);
-  for (long long step = blockIdx.x; step < steps; step += gridDim.x) {
-    if (step < qsteps) {
-      const int t = (int)step * kSideRows + row;
-      if (t >= a.total_q || t >= __ldg(a.cu_q + a.batch) || t < __ldg(a.cu_q)) continue;
+  for (int j = threadIdx.x; j < half; j += kSideThreads) s_freq[j] = j < a.r ? rope_inv_freq_turns(j, d, a.log2_base) : 0.0;
+  __syncthreads();
+  const int rot_groups = min(groups, (a.r + 63) / 64 * 8);   // whole 64-dim chunks
+  const int qh = (a.hq + kSideQHeads - 1) / kSideQHeads, kh = (hkv + kSideHeads - 1) / kSideHeads;
+  const int kg = E4M3 ? groups : rot_groups;
+  const long long nq = p.q_mask ? (long long)a.total_q * qh * rot_groups : 0;
+  const long long nk = E4M3 || p.k_mask ? (long long)p.tile0[a.batch] * kCN * kh * kg : 0;
+  const long long ne = E4M3 ? 0 : (long long)a.batch * 2 * kCN * kh * groups;
+  auto angles = [&](int pos, int j0, float* c, float* s) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      c[e] = 1.f;
+      s[e] = 0.f;
+      if (j0 + e < a.r) rope_cos_sin((double)pos, s_freq[j0 + e], &c[e], &s[e]);
+    }
+  };
+  for (long long i = (long long)blockIdx.x * kSideThreads + threadIdx.x; i < nq + nk + ne; i += (long long)gridDim.x * kSideThreads) {
+    if (i < nq) {
+      const int g = (int)(i % rot_groups), j0 = 8 * g;
+      const int h0 = (int)(i / rot_groups % qh) * kSideQHeads, t = (int)(i / rot_groups / qh);
+      if (t >= __ldg(a.cu_q + a.batch) || t < __ldg(a.cu_q)) continue;
       const int b = seq_of_row(a.cu_q, a.batch, t);
       if (p.chunk_of[b] < 0) continue;
-      const double pos = (double)(__ldg(a.lens + b) + t - __ldg(a.cu_q + b));
-      for (int g = lane8; g < groups; g += 8) {
-        const int j0 = 8 * g, c0 = chunk_col(p.q_mask, j0), c1 = chunk_col(p.q_mask, j0 + half);
-        if (c0 < 0 && c1 < 0) continue;
-        float c[8], s[8];
+      const int c0 = chunk_col(p.q_mask, j0), c1 = chunk_col(p.q_mask, j0 + half);
+      float c[8], s[8];
+      angles(__ldg(a.lens + b) + t - __ldg(a.cu_q + b), j0, c, s);
+#pragma unroll 1
+      for (int h = h0; h < min(h0 + kSideQHeads, a.hq); h += kSideHeads) {
+        const size_t row = (size_t)t * a.hq + h;
+        uint4 w0[kSideHeads], w1[kSideHeads];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          c[e] = 1.f;
-          s[e] = 0.f;
-          if (j0 + e < a.r) rope_cos_sin(pos, rope_inv_freq_turns(j0 + e, d, a.log2_base), &c[e], &s[e]);
+        for (int k = 0; k < kSideHeads; ++k) {
+          if (h + k >= a.hq) break;
+          w0[k] = __ldg(reinterpret_cast<const uint4*>(a.q + (row + k) * d + j0));
+          w1[k] = __ldg(reinterpret_cast<const uint4*>(a.q + (row + k) * d + j0 + half));
         }
-        for (int h = 0; h < a.hq; ++h) {
-          const uint16_t* src = a.q + ((size_t)t * a.hq + h) * d;
-          uint16_t* dst = p.q_side + ((size_t)t * a.hq + h) * p.q_cols;
+#pragma unroll
+        for (int k = 0; k < kSideHeads; ++k) {
+          if (h + k >= a.hq) break;
           float x0[8], x1[8], y0[8], y1[8];
-          bf8_to_f32(__ldg(reinterpret_cast<const uint4*>(src + j0)), x0);
-          bf8_to_f32(__ldg(reinterpret_cast<const uint4*>(src + j0 + half)), x1);
+          bf8_to_f32(w0[k], x0);
+          bf8_to_f32(w1[k], x1);
           turn8(x0, x1, c, s, y0, y1);
+          uint16_t* dst = p.q_side + (row + k) * p.q_cols;
           if (c0 >= 0) *reinterpret_cast<uint4*>(dst + c0) = f32_to_bf8(y0);
           if (c1 >= 0) *reinterpret_cast<uint4*>(dst + c1) = f32_to_bf8(y1);
         }
       }
       continue;
     }
-    const int tile = (int)((step - qsteps) / (kCN / kSideRows));
-    const int in_tile = (int)((step - qsteps) % (kCN / kSideRows)) * kSideRows + row;
-    int b = 0, y = a.batch;
-    while (y - b > 1) {
-      const int m = (b + y) >> 1;
-      if (p.tile0[m] <= tile) b = m;
-      else y = m;
+    const bool edges = i >= nq + nk;
+    const long long ik = edges ? i - nq - nk : i - nq;
+    const int gs = edges ? groups : kg;
+    const int g = (int)(ik % gs), j0 = 8 * g, h = (int)(ik / gs % kh) * kSideHeads;
+    const long long row = ik / gs / kh;
+    const int in_tile = (int)(row % kCN), tile = (int)(row / kCN);
+    int b = 0, kt;
+    if (edges) {
+      b = tile >> 1;
+      if (p.chunk_of[b] < 0) continue;
+      kt = 0;
+    } else {
+      int y = a.batch;  // the last sequence with tile0 <= tile (those without tiles share a value)
+      while (y - b > 1) {
+        const int m = (b + y) >> 1;
+        if (p.tile0[m] <= tile) b = m;
+        else y = m;
+      }
+      kt = tile - p.tile0[b];
     }
-    const int n = __ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b), len = __ldg(a.lens + b);
-    const int first = keys_first(a, len, 0), end = len + n;
-    const int kt = first / kCN + tile - p.tile0[b];
-    const bool head_cut = kt * kCN < first, tail_cut = (kt + 1) * kCN > end;
-    const bool copy = E4M3 || head_cut || tail_cut;
-    if (!copy && !p.k_mask) continue;
+    const int len = __ldg(a.lens + b), end = len + __ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b);
+    const int first = keys_first(a, len, 0);
+    kt = edges && (tile & 1) ? (end - 1) / kCN : first / kCN + kt;
+    // The copy of the first tile is the first of two, unless it is the last one too.
+    if (edges && ((tile & 1) ? (kt + 1) * kCN == end : kt * kCN == first || (kt + 1) * kCN > end)) continue;
     const int pos = kt * kCN + in_tile;
     bool have = pos >= first && pos < end;
     size_t src = 0;
     if (have) {
       const int page = page_of(a.c, b, pos >> a.c.page_shift);
       have = page >= 0;
-      src = have ? page_row(a.c, page, 0, pos & ((1 << a.c.page_shift) - 1)) : 0;
+      src = have ? page_row(a.c, page, h, pos & ((1 << a.c.page_shift) - 1)) : 0;
     }
     const size_t head_step = (size_t)1 << a.c.page_shift;
-    const size_t side_row = (size_t)tile * kCN + in_tile;
-    const size_t copy_row = E4M3 ? side_row : ((size_t)2 * p.chunk_of[b] + (tail_cut ? 1 : 0)) * kCN + in_tile;
-    const int esz = E4M3 ? 1 : 2;
-    for (int g = lane8; g < groups; g += 8) {
-      const int j0 = 8 * g, c0 = chunk_col(p.k_mask, j0), c1 = chunk_col(p.k_mask, j0 + half);
-      const bool rot = c0 >= 0 || c1 >= 0;
-      if (!rot && !copy) continue;
-      float c[8], s[8];
-      if (rot) {
+    const int c0 = edges ? -1 : chunk_col(p.k_mask, j0), c1 = edges ? -1 : chunk_col(p.k_mask, j0 + half);
+    const long long copy_row = edges ? ((long long)2 * p.chunk_of[b] + (tile & 1)) * kCN + in_tile : row;
+    const bool copy = E4M3 || edges;
+    // The rows of the heads: K, and where they are copied V, as they lie.
+    using Raw = typename std::conditional<E4M3, uint2, uint4>::type;
+    auto fetch = [&](const uint8_t* pool, Raw* w0, Raw* w1) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          c[e] = 1.f;
-          s[e] = 0.f;
-          if (j0 + e < a.r) rope_cos_sin((double)pos, rope_inv_freq_turns(j0 + e, d, a.log2_base), &c[e], &s[e]);
-        }
+      for (int k = 0; k < kSideHeads; ++k) {
+        const uint8_t* at = pool + ((src + k * head_step) * d + j0) * (E4M3 ? 1 : 2);
+        const bool get = have && h + k < hkv;
+        w0[k] = get ? __ldg(reinterpret_cast<const Raw*>(at)) : Raw{};
+        w1[k] = get ? __ldg(reinterpret_cast<const Raw*>(at + half * (E4M3 ? 1 : 2))) : Raw{};
       }
-      for (int h = 0; h < hkv; ++h) {
-        float x0[8] = {}, x1[8] = {}, y0[8], y1[8];
-        const size_t at = src + h * head_step;
-        if (have) {
-          const float sc = E4M3 ? __ldg(a.c.k_scales + at) : 1.f;
-          load8<E4M3>(a.c.k + at * d * esz, j0, sc, x0);
-          load8<E4M3>(a.c.k + at * d * esz, j0 + half, sc, x1);
+    };
+    auto widen = [&](Raw w, float scale, float* f) {
+      if constexpr (E4M3) {
+        e4m3x4_to_f32(w.x, f);
+        e4m3x4_to_f32(w.y, f + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= scale;
+      } else {
+        bf8_to_f32(w, f);
+      }
+    };
+    auto scale_of = [&](const float* scales, int k) { return E4M3 && have && h + k < hkv ? __ldg(scales + src + k * head_step) : 0.f; };
+    {
+      Raw w0[kSideHeads], w1[kSideHeads];
+      float sc[kSideHeads], c[8], s[8];
+      fetch(a.c.k, w0, w1);
+#pragma unroll
+      for (int k = 0; k < kSideHeads; ++k) sc[k] = scale_of(a.c.k_scales, k);
+      if (c0 >= 0 || c1 >= 0) angles(pos, j0, c, s);
+#pragma unroll
+      for (int k = 0; k < kSideHeads; ++k) {
+        if (h + k >= hkv) break;
+        float x0[8], x1[8], y0[8], y1[8];
+        widen(w0[k], sc[k], x0);
+        widen(w1[k], sc[k], x1);
+        if (copy) {
+          uint16_t* dst = p.k_copy + ((size_t)(h + k) * p.copy_rows + copy_row) * d + j0;
+          *reinterpret_cast<uint4*>(dst) = f32_to_bf8(x0);
+          *reinterpret_cast<uint4*>(dst + half) = f32_to_bf8(x1);
         }
-        if (rot) {
-          uint16_t* dst = p.k_rot + ((size_t)h * p.rot_rows + side_row) * p.k_cols;
+        if (c0 >= 0 || c1 >= 0) {
+          uint16_t* dst = p.k_rot + ((size_t)(h + k) * p.rot_rows + row) * p.k_cols;
           turn8(x0, x1, c, s, y0, y1);
           if (c0 >= 0) *reinterpret_cast<uint4*>(dst + c0) = f32_to_bf8(y0);
           if (c1 >= 0) *reinterpret_cast<uint4*>(dst + c1) = f32_to_bf8(y1);
         }
-        if (copy) {
-          uint16_t* dst = p.k_copy + ((size_t)h * p.copy_rows + copy_row) * d;
-          *reinterpret_cast<uint4*>(dst + j0) = f32_to_bf8(x0);
-          *reinterpret_cast<uint4*>(dst + j0 + half) = f32_to_bf8(x1);
-          if (a.c.v != nullptr) {
-            float v0[8] = {}, v1[8] = {};
-            if (have) {
-              const float sc = E4M3 ? __ldg(a.c.v_scales + at) : 1.f;
-              load8<E4M3>(a.c.v + at * d * esz, j0, sc, v0);
-              load8<E4M3>(a.c.v + at * d * esz, j0 + half, sc, v1);
-            }
-            dst = p.v_copy + ((size_t)h * p.copy_rows + copy_row) * d;
-            *reinterpret_cast<uint4*>(dst + j0) = f32_to_bf8(v0);
-            *reinterpret_cast<uint4*>(dst + j0 + half) = f32_to_bf8(v1);
-          }
-        }
+      }
+    }
+    if (copy && a.c.v != nullptr) {
+      Raw w0[kSideHeads], w1[kSideHeads];
+      float sc[kSideHeads];
+      fetch(a.c.v, w0, w1);
+#pragma unroll
+      for (int k = 0; k < kSideHeads; ++k) sc[k] = scale_of(a.c.v_scales, k);
+#pragma unroll
+      for (int k = 0; k < kSideHeads; ++k) {
+        if (h + k >= hkv) break;
+        float x0[8], x1[8];
+        widen(w0[k], sc[k], x0);
+        widen(w1[k], sc[k], x1);
+        uint16_t* dst = p.v_copy + ((size_t)(h + k) * p.copy_rows + copy_row) * d + j0;
+        *reinterpret_cast<uint4*>(dst) = f32_to_bf8(x0);
+        *reinterpret_cast<uint4*>(dst + half) = f32_to_bf8(x1);
       }
     }
   }
@@ -476,130 +512,158 @@ chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ Pag
   volatile int* abort_flag = &bars->abort_flag;
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer (whole warp: a lane per box)
-    auto expect = [&](uint64_t* bar, uint32_t bytes) {
-      if (!PAIR || leader) mbar_arrive_expect_tx(bar, bytes);
-      else mbar_arrive_expect_tx_cluster(smem_u32(bar) & kPeerBitMask, bytes);
-    };
-    auto load = [&](void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
-      if constexpr (PAIR) tma_load_3d_pair(dst, map, bar, c0, c1, c2);
-      else tma_load_3d(dst, map, bar, c0, c1, c2);
-    };
-    auto col_of = [](uint32_t mask, int c) { return __popc(mask & ((1u << c) - 1u)) * 64; };
-    const int ps = 1 << a.c.page_shift;
-    const int kbox = min(ps, Cfg::kKeys), vbox = min(ps, kCN);      // rows of a page box
-    const int kboxes = Cfg::kKeys / kbox, vboxes = kCN / vbox;
-    const int out_plane = a.c.num_pages * a.c.hkv;                  // past the pool: a box of zeros
-    int st = 0;
-    uint32_t ph = 0;
-    auto next = [&]() { if (++st == Cfg::kStages) { st = 0; ph ^= 1u; } };
-    bool ok = true;
-    int unit_iter = 0, q_issued = 0;
-    for (int r = 0; r < nrounds && ok; ++r) {
-      Unit w;
-      if (!unit_of_round(r, w)) continue;
-      if (w.ntiles == 0) continue;
-      if (unit_iter > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (uint32_t)(unit_iter - 1) & 1u, abort_flag));
-        if (!ok) break;
-      }
-      if (lane == 0) expect(&bars->q_full, Cfg::kQChunks * 128u * (uint32_t)(tpc * a.group));
-      __syncwarp();
-      if (lane < Cfg::kQChunks) {
-        const int c = lane;
-        const bool rot = (p.q_mask >> c) & 1u;
-        load(q_smem + c * kCChunkBytes, rot ? &maps.qs : &maps.q, &bars->q_full, rot ? col_of(p.q_mask, c) : c * 64,
-             w.kvh * a.group, w.tok0 + w.t0 + (int)rank * tpc);
-      }
-      ++q_issued;
-      const int first = keys_first(a, w.len, 0), end = w.len + w.n, seq_kt0 = first / kCN;
-      const int side0 = p.tile0[w.b];
-      const int edge0 = 2 * p.chunk_of[w.b];
-      // Rows of tile kt in the copies: -1 when the tile is read from the pages.
-      auto copy_row = [&](int kt) -> int {
-        if (p.e4m3) return (side0 + kt - seq_kt0) * kCN;
-        if ((kt + 1) * kCN > end) return (edge0 + 1) * kCN;
-        if (kt * kCN < first) return edge0 * kCN;
-        return -1;
+    // ------------------------------------------------------------ producer
+    // One thread, by elect.sync: a copy issued by divergent lanes costs some 200 cycles, and with
+    // pages of 16 a tile takes 32 boxes.
+    if (elect_one()) {
+      auto expect = [&](uint64_t* bar, uint32_t bytes) {
+        if (!PAIR || leader) mbar_arrive_expect_tx(bar, bytes);
+        else mbar_arrive_expect_tx_cluster(smem_u32(bar) & kPeerBitMask, bytes);
       };
-      // Plane (page, head) of position pos, for interior tiles.
-      auto plane_of = [&](int pos) -> int {
-        const int pg = page_of(a.c, w.b, pos >> a.c.page_shift);
-        return pg < 0 ? out_plane : pg * a.c.hkv + w.kvh;
+      auto load = [&](void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+        if constexpr (PAIR) tma_load_3d_pair(dst, map, bar, c0, c1, c2);
+        else tma_load_3d(dst, map, bar, c0, c1, c2);
       };
-      // The table entries of a tile are read one tile ahead: this lane's box of the next K
-      // stages and of the next V stages.
-      const int kpos = (int)rank * (PAIR ? 64 : 0) + (lane % kboxes) * kbox, vpos = (lane % vboxes) * vbox;
-      auto k_plane = [&](int kt) { return copy_row(kt) < 0 ? plane_of(kt * kCN + kpos) : 0; };
-      auto v_plane = [&](int kt) { return copy_row(kt) < 0 ? plane_of(kt * kCN + vpos) : 0; };
-      int kpl = k_plane(w.kt_lo), vpl = 0, vpl_next = v_plane(w.kt_lo);
-      for (int jj = 0; jj <= w.ntiles && ok; ++jj) {
-        if (jj < w.ntiles) {
-          const int kt = w.kt_lo + jj, cr = copy_row(kt);
-          const int kpl_next = jj + 1 < w.ntiles ? k_plane(kt + 1) : 0;
-          for (int s = 0; s < Cfg::kKStages && ok; ++s) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->ring_empty[st], ph ^ 1u, abort_flag));
-            if (!ok) break;
-            uint64_t* bar = &bars->ring_full[st];
-            if (lane == 0) expect(bar, Cfg::kStageBytes);
-            __syncwarp();
-            uint8_t* dst = ring + st * Cfg::kStageBytes;
-            // lanes [0, kKPerStage * kboxes): chunk sub = lane / kboxes, box lane % kboxes
-            const int sub = lane / kboxes, box = lane % kboxes;
-            if (sub < Cfg::kKPerStage) {
-              const int c = Cfg::kKPerStage * s + sub;
-              uint8_t* d0 = dst + sub * Cfg::kKChunkBytes;
-              if ((p.k_mask >> c) & 1u) {
-                if (box == 0)
-                  load(d0, &maps.k_rot, bar, col_of(p.k_mask, c), (side0 + kt - seq_kt0) * kCN + (int)rank * (PAIR ? 64 : 0), w.kvh);
-              } else if (cr >= 0) {
-                if (box == 0) load(d0, &maps.k_copy, bar, c * 64, cr + (int)rank * (PAIR ? 64 : 0), w.kvh);
-              } else {
-                load(d0 + box * kbox * 128, &maps.k, bar, c * 64, (kt * kCN + kpos) & (ps - 1), kpl);
-              }
-            }
-            next();
-          }
-          kpl = kpl_next;
+      auto col_of = [](uint32_t mask, int c) { return __popc(mask & ((1u << c) - 1u)) * 64; };
+      const int ps = 1 << a.c.page_shift;
+      const int kbox = min(ps, Cfg::kKeys), vbox = min(ps, kCN);      // rows of a page box
+      const int kboxes = Cfg::kKeys / kbox, vboxes = kCN / vbox;
+      const int k_off = (int)rank * (PAIR ? 64 : 0);                  // this CTA's keys of a K tile
+      int st = 0;
+      uint32_t ph = 0;
+      auto next = [&]() { if (++st == Cfg::kStages) { st = 0; ph ^= 1u; } };
+      bool ok = true;
+      int unit_iter = 0, q_issued = 0;
+      for (int r = 0; r < nrounds && ok; ++r) {
+        Unit w;
+        if (!unit_of_round(r, w)) continue;
+        if (w.ntiles == 0) continue;
+        if (unit_iter > 0) {
+          ok = mbar_wait(&bars->q_empty, (uint32_t)(unit_iter - 1) & 1u, abort_flag);
+          if (!ok) break;
         }
-        if (jj >= 1) {
-          const int kt = w.kt_lo + jj - 1, cr = copy_row(kt);
-          vpl = vpl_next;
-          if (jj < w.ntiles) vpl_next = v_plane(kt + 1);
-          for (int s = 0; s < Cfg::kVStages && ok; ++s) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->ring_empty[st], ph ^ 1u, abort_flag));
-            if (!ok) break;
-            uint64_t* bar = &bars->ring_full[st];
-            if (lane == 0) expect(bar, Cfg::kStageBytes);
-            __syncwarp();
-            const int sub = lane / vboxes, box = lane % vboxes;
-            if (sub < Cfg::kVPerStage) {
-              const int c = ((PAIR ? 2 * s + (int)rank : s) * Cfg::kVPerStage) + sub;
-              uint8_t* d0 = ring + st * Cfg::kStageBytes + sub * kCChunkBytes;
+        expect(&bars->q_full, Cfg::kQChunks * 128u * (uint32_t)(tpc * a.group));
+#pragma unroll 1
+        for (int c = 0; c < Cfg::kQChunks; ++c) {
+          const bool rot = (p.q_mask >> c) & 1u;
+          load(q_smem + c * kCChunkBytes, rot ? &maps.qs : &maps.q, &bars->q_full, rot ? col_of(p.q_mask, c) : c * 64,
+               w.kvh * a.group, w.tok0 + w.t0 + (int)rank * tpc);
+        }
+        ++q_issued;
+        const int first = keys_first(a, w.len, 0), end = w.len + w.n, seq_kt0 = first / kCN;
+        const int side0 = p.tile0[w.b];
+        const int edge0 = 2 * p.chunk_of[w.b];
+        // Rows of tile kt in the copies: -1 when the tile is read from the pages.
+        auto copy_row = [&](int kt) -> int {
+          if (p.e4m3) return (side0 + kt - seq_kt0) * kCN;
+          if ((kt + 1) * kCN > end) return (edge0 + 1) * kCN;
+          if (kt * kCN < first) return edge0 * kCN;
+          return -1;
+        };
+        // Table entries of a tile's boxes are read one tile ahead, and looked at when they are used.
+        const int32_t* table = a.c.table + (size_t)w.b * a.c.max_blocks;
+        auto entries = [&](int kt, int off, int box, int count, int most, int* e) {
+          const bool pages = copy_row(kt) < 0;
+#pragma unroll
+          for (int i = 0; i < most; ++i)
+            e[i] = pages && i < count ? __ldg(table + ((kt * kCN + off + i * box) >> a.c.page_shift)) : 0;
+        };
+        // Plane (page, head); a bad page's is past the pool, where a box reads zeros.
+        auto plane_of = [&](int e) -> int {
+          if ((unsigned)e >= (unsigned)a.c.num_pages) {
+            atomicOr(&g_status, kStatusPage);
+            return a.c.num_pages * a.c.hkv;
+          }
+          return e * a.c.hkv + w.kvh;
+        };
+        constexpr int KB = Cfg::kKeys / 16, VB = kCN / 16;
+        int ke[KB], ke_next[KB], ve[VB], ve_next[VB];
+        entries(w.kt_lo, k_off, kbox, kboxes, KB, ke_next);
+        entries(w.kt_lo, 0, vbox, vboxes, VB, ve_next);
+#pragma unroll 1
+        for (int jj = 0; jj <= w.ntiles && ok; ++jj) {
+          if (jj < w.ntiles) {
+            const int kt = w.kt_lo + jj, cr = copy_row(kt);
+            const int k_row = kt * kCN + k_off;
+#pragma unroll
+            for (int i = 0; i < KB; ++i) ke[i] = plane_of(ke_next[i]);
+            if (jj + 1 < w.ntiles) entries(kt + 1, k_off, kbox, kboxes, KB, ke_next);
+#pragma unroll 1
+            for (int s = 0; s < Cfg::kKStages; ++s) {
+              ok = mbar_wait(&bars->ring_empty[st], ph ^ 1u, abort_flag);
+              if (!ok) break;
+              uint64_t* bar = &bars->ring_full[st];
+              expect(bar, Cfg::kStageBytes);
+              uint8_t* dst = ring + st * Cfg::kStageBytes;
+              const int c0 = Cfg::kKPerStage * s;
+              const uint32_t side = cr >= 0 ? ~0u : p.k_mask >> c0;  // chunks that are not read from the pages
+#pragma unroll
+              for (int i = 0; i < KB; ++i) {
+                if (i >= kboxes) break;
+#pragma unroll
+                for (int sub = 0; sub < Cfg::kKPerStage; ++sub)
+                  if (!((side >> sub) & 1u))
+                    load(dst + sub * Cfg::kKChunkBytes + i * kbox * 128, &maps.k, bar, (c0 + sub) * 64,
+                         (k_row + i * kbox) & (ps - 1), ke[i]);
+              }
+#pragma unroll 1
+              for (int sub = 0; sub < Cfg::kKPerStage; ++sub) {
+                if (!((side >> sub) & 1u)) continue;
+                uint8_t* at = dst + sub * Cfg::kKChunkBytes;
+                if ((p.k_mask >> (c0 + sub)) & 1u)
+                  load(at, &maps.k_rot, bar, col_of(p.k_mask, c0 + sub), (side0 + kt - seq_kt0) * kCN + k_off, w.kvh);
+                else
+                  load(at, &maps.k_copy, bar, (c0 + sub) * 64, cr + k_off, w.kvh);
+              }
+              next();
+            }
+          }
+          if (jj >= 1 && ok) {
+            const int kt = w.kt_lo + jj - 1, cr = copy_row(kt);
+#pragma unroll
+            for (int i = 0; i < VB; ++i) ve[i] = plane_of(ve_next[i]);
+            if (jj < w.ntiles) entries(kt + 1, 0, vbox, vboxes, VB, ve_next);
+#pragma unroll 1
+            for (int s = 0; s < Cfg::kVStages; ++s) {
+              ok = mbar_wait(&bars->ring_empty[st], ph ^ 1u, abort_flag);
+              if (!ok) break;
+              uint64_t* bar = &bars->ring_full[st];
+              expect(bar, Cfg::kStageBytes);
+              uint8_t* dst = ring + st * Cfg::kStageBytes;
+              const int col = w.part * Cfg::kDv + (PAIR ? 2 * s + (int)rank : s) * Cfg::kVPerStage * 64;
               if (cr >= 0) {
-                if (box == 0) load(d0, &maps.v_copy, bar, w.part * Cfg::kDv + c * 64, cr, w.kvh);
+#pragma unroll
+                for (int sub = 0; sub < Cfg::kVPerStage; ++sub)
+                  load(dst + sub * kCChunkBytes, &maps.v_copy, bar, col + sub * 64, cr, w.kvh);
               } else {
-                load(d0 + box * vbox * 128, &maps.v, bar, w.part * Cfg::kDv + c * 64, (kt * kCN + vpos) & (ps - 1), vpl);
+#pragma unroll
+                for (int i = 0; i < VB; ++i) {
+                  if (i >= vboxes) break;
+#pragma unroll
+                  for (int sub = 0; sub < Cfg::kVPerStage; ++sub)
+                    load(dst + sub * kCChunkBytes + i * vbox * 128, &maps.v, bar, col + sub * 64, (kt * kCN + i * vbox) & (ps - 1),
+                         ve[i]);
+                }
               }
+              next();
             }
-            next();
           }
         }
+        ++unit_iter;
       }
-      ++unit_iter;
-    }
-    // Copies counted on this CTA's barriers land before it can leave: the last fill of each
-    // slot (its phase has parity ph ^ 1 in the order walked here) and the last Q. The odd CTA's
-    // copies complete on the even CTA's barriers, which waits for them before the pair leaves.
-    if (lane == 0 && (!PAIR || leader)) {
-      for (int s = 0; s < Cfg::kStages; ++s) {
-        const unsigned long long w0 = globaltimer_ns();
-        while (!mbar_try_wait(&bars->ring_full[st], ph ^ 1u) && globaltimer_ns() - w0 < kWaitLimitNs) {}
-        next();
-      }
-      if (q_issued > 0) {
-        const unsigned long long w0 = globaltimer_ns();
-        while (!mbar_try_wait(&bars->q_full, (uint32_t)(q_issued - 1) & 1u) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+      // Copies counted on this CTA's barriers land before it can leave: the last fill of each
+      // slot (its phase has parity ph ^ 1 in the order walked here) and the last Q. The odd CTA's
+      // copies complete on the even CTA's barriers, which waits for them before the pair leaves.
+      if (!PAIR || leader) {
+        for (int s = 0; s < Cfg::kStages; ++s) {
+          const unsigned long long w0 = globaltimer_ns();
+          while (!mbar_try_wait(&bars->ring_full[st], ph ^ 1u) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+          next();
+        }
+        if (q_issued > 0) {
+          const unsigned long long w0 = globaltimer_ns();
+          while (!mbar_try_wait(&bars->q_full, (uint32_t)(q_issued - 1) & 1u) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+        }
       }
     }
     __syncwarp();

@@ -813,78 +813,73 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
 
 // ---------------------------------------------------------------------------
 // Join of cut units: out = sum_s exp(lse_s - M) o_s / sum_s exp(lse_s - M) over the teams whose runs
-// the unit crosses, in order. A warp takes 128 columns of one row, four per lane.
+// the unit crosses, in order. A block takes a border between two runs; the unit that it cuts is
+// joined there if no earlier border cuts it. A warp takes 128 columns of one row, four per lane.
+// (Walking all rows of the call instead, to find the few of cut units, took 167 us of a call of
+// three prompt chunks, which has none.)
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) paged_merge_kernel(PagedAttendArgs a) {
   const int lane = threadIdx.x & 31;
-  const int D = a.c.d, chunks = (D + 127) / 128;
-  const long long wid = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const long long row = wid / chunks;
-  if (row >= (long long)a.total_q * a.hq) return;
-  const int c0 = (int)(wid % chunks) * 128 + lane * 4;
-  const int tok = (int)(row / a.hq), head = (int)(row % a.hq);
-  if (tok >= __ldg(a.cu_q + a.batch) || tok < __ldg(a.cu_q)) return;
-  const int b = seq_of_row(a.cu_q, a.batch, tok);
-  int blocks, units;
-  seq_units(a, b, &blocks, &units);
-  if (units == 0) return;
-  // units and blocks before this sequence, and in all
-  int before = 0, total = 0;
-  for (int i = lane; i < a.batch; i += 32) {
-    int bl, un;
-    seq_units(a, i, &bl, &un);
-    total += bl * un;
-    if (i < b) before += bl * un;
-  }
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, m);
-    before += __shfl_xor_sync(0xffffffffu, before, m);
-  }
+  const int D = a.c.d, ur = a.unit_rows, chunks = (D + 127) / 128;
+  int b, before, blocks, units;
+  const int total = line_find(a, lane, -1, &b, &before);
   const int run = run_length(a, total);
-  const int in_head = (tok - __ldg(a.cu_q + b)) * a.group + head % a.group;  // row within the KV head
-  const int ur = a.unit_rows, u = in_head / ur * a.c.hkv + head / a.group;
-  if (u >= units) return;
-  const int x0 = before + u * blocks, x1 = x0 + blocks;
-  const int w0 = x0 / run, w1 = (x1 - 1) / run;
-  if (w0 == w1) return;  // one team had it all, and wrote the output
-  auto at = [&](int w) { return ((size_t)2 * w + (w == w0 ? 1 : 0)) * ur + in_head % ur; };
-  float mm = -INFINITY;
-  bool nan = false;
-  for (int w = w0 + lane; w <= w1; w += 32) {
-    const float l = a.partial_lse[at(w)];
-    nan |= l != l;
-    mm = fmaxf(mm, l);
-  }
+  const long long x = (long long)(blockIdx.x + 1) * run;  // the border
+  if (x >= total) return;
+  line_find(a, lane, (int)x, &b, &before);
+  seq_units(a, b, &blocks, &units);
+  const int u = ((int)x - before) / blocks, x0 = before + u * blocks, w0 = x0 / run;
+  if (x0 == x || w0 != (int)blockIdx.x) return;  // nothing is cut, or an earlier border joins it
+  const int w1 = (x0 + blocks - 1) / run;
+  const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0;
+  const int row0 = u / a.c.hkv * ur, rows = min(ur, n * a.group - row0);
+#pragma unroll 1
+  for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < rows * chunks; i += gridDim.y * 8) {
+    const int ri = i / chunks, c0 = i % chunks * 128 + lane * 4, in_head = row0 + ri;  // row within the KV head
+    const int tk = in_head / a.group;
+    const size_t row = ((size_t)tok0 + tk) * a.hq + u % a.c.hkv * a.group + (in_head - tk * a.group);
+    auto at = [&](int w) { return ((size_t)2 * w + (w == w0 ? 1 : 0)) * ur + ri; };
+    // Up to 32 parts at a time, a lane each; the reference is the largest of those seen so far.
+    float mm = -INFINITY, den = 0.f, bad = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int wb = w0; wb <= w1; wb += 32) {
+      const float l = wb + lane <= w1 ? a.partial_lse[at(wb + lane)] : -INFINITY;
+      if (__any_sync(0xffffffffu, l != l)) bad = NAN;
+      float m = fmaxf(mm, l);
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, m));
-  nan = __any_sync(0xffffffffu, nan);
-  float den = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+      if (m == -INFINITY) continue;
+      const float old = __expf(mm - m), mine = l > -INFINITY ? __expf(l - m) : 0.f;
+      mm = m;
+      den *= old;
+      acc.x *= old; acc.y *= old; acc.z *= old; acc.w *= old;
+      const uint32_t live = __ballot_sync(0xffffffffu, l > -INFINITY);  // an empty part's output is not written
+      const int count = min(32, w1 - wb + 1);
 #pragma unroll 4
-  for (int w = w0; w <= w1; ++w) {
-    const float l = a.partial_lse[at(w)];
-    if (l == -INFINITY) continue;
-    const float wt = nan ? l : __expf(l - mm);
-    den += wt;
-    if (c0 < D) {
-      const float4 v = *reinterpret_cast<const float4*>(a.partial_o + at(w) * D + c0);
-      acc.x += wt * v.x; acc.y += wt * v.y; acc.z += wt * v.z; acc.w += wt * v.w;
+      for (int k = 0; k < count; ++k) {
+        const float wt = __shfl_sync(0xffffffffu, mine, k);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (((live >> k) & 1u) && c0 < D) v = __ldg(reinterpret_cast<const float4*>(a.partial_o + at(wb + k) * D + c0));
+        den += wt;
+        acc.x = fmaf(wt, v.x, acc.x); acc.y = fmaf(wt, v.y, acc.y); acc.z = fmaf(wt, v.z, acc.z); acc.w = fmaf(wt, v.w, acc.w);
+      }
     }
+    den += bad;
+    if (c0 < D) {
+      const float inv = den > 0.f || den != den ? 1.f / den : 0.f;
+      acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;  // a NaN den makes them NaN
+      const size_t o = row * D + c0;
+      if (a.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = acc;
+      else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    }
+    if (c0 == 0 && a.lse) a.lse[row] = den != den ? den : mm == -INFINITY ? -INFINITY : mm + logf(den);
   }
-  if (c0 < D) {
-    const float inv = den > 0.f || den != den ? 1.f / den : 0.f;
-    acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
-    const size_t o = (size_t)row * D + c0;
-    if (a.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = acc;
-    else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-  }
-  if (c0 == 0 && a.lse) a.lse[row] = den != den ? den : mm == -INFINITY ? -INFINITY : mm + logf(den);
 }
 
 cudaError_t launch_paged_merge(const PagedAttendArgs& a, cudaStream_t stream) {
-  const long long warps = (long long)a.total_q * a.hq * ((a.c.d + 127) / 128);
-  paged_merge_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(a);
+  if (a.teams < 2) return cudaSuccess;
+  const dim3 grid(a.teams - 1, (a.unit_rows * ((a.c.d + 127) / 128) + 31) / 32);  // up to four rows' columns a warp
+  paged_merge_kernel<<<grid, 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
