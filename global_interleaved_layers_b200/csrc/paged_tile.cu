@@ -48,7 +48,8 @@ namespace gattn {
 namespace {
 
 constexpr int kTThreads = 512;
-constexpr int kTMaxSlots = 28;
+constexpr int kTSlotBytes = 16384;     // of a ring slot: one 128-byte column chunk of 128 keys, or two of 64
+constexpr int kTMaxSlots = 14;
 constexpr float kTop8 = 7.f;           // e4m3: the running maximum's weight is 2^7,
 constexpr float kHeadroom8 = 1.75f;    // others up to 2^8.75 < 448
 
@@ -67,14 +68,15 @@ struct __align__(16) TileHeader {
   uint64_t rot_in[4];       // the producer has started the loads of a tile's rotated chunks
   uint64_t rot_ready[2];
   uint64_t s_full[2], p_full[2], pv_done[2];
-  uint64_t o_empty, hmeet[2], mma_done[2];
+  uint64_t o_empty, o_meet, hmeet[2], mma_done[2];
   uint64_t piece_full[8], piece_empty[8];
   uint32_t tmem_base;
   int abort_flag;
-  int viol[2][SG][4];
-  float red[2][SG][2][4][H <= 8 ? 8 : 32];  // [meeting parity][group][maxima or weights' maxima][quadrant][row]
-  float step[SG][2][H];     // a group's factors for sums and output when its references move
-  float refs[2][SG][2][H];  // [unit parity][softmax group]: references of the sums and of the weights
+  alignas(16) int viol[2][2][4];  // [meeting parity][softmax group][quadrant]
+  alignas(16) float red[2][2][2][4][H <= 8 ? 8 : 32];  // [meeting parity][group][maxima or weights' maxima][quadrant][row]
+  float sums[2][2][4][H <= 8 ? 8 : 32];    // [unit parity][group][quadrant][row]
+  float step[2][2][H];      // a group's factors for sums and output when its references move
+  float refs[2][2][2][H];   // [unit parity][group]: references of the sums and of the weights
   float qsc[4][SG * H];         // e4m3: score factor of a unit's rows (unit mod 4)
   int orow[4][SG * H];          // output row (token x query heads + head) of a unit's rows
   int qpos[4][SG * H];          // and their positions
@@ -82,18 +84,23 @@ struct __align__(16) TileHeader {
   double itf[64];           // theta_j / (2 pi), 0 past the rotated pairs
 };
 
-// Shape of a CTA for units of NR = SG * H rows: SG softmax groups, H rows a thread.
+// Shape of a CTA for units of NR = SG * H rows. Two softmax groups: with SG = 2 each has half of
+// the rows, with SG = 1 every other tile (and an output of its own, joined at the end).
 template <int D, bool E4M3, int SG, int H>
 struct TileCfg {
   static constexpr int KT = (!E4M3 && D == 512) ? 64 : 128;   // keys per tile
   static constexpr int NR = SG * H;                           // rows of a unit
-  static constexpr int HW = SG == 1 ? 8 : 4;                  // warps for query rows and rotation
+  static constexpr int TG = 3 - SG;                           // groups that share the rows
+  static constexpr int HW = 4;                                // warps for query rows and rotation
   // columns: the MMA's N, in 16s (8s with 64 keys on M, for the scores: NQ below)
   static constexpr int N = E4M3 ? (2 * NR + 15) / 16 * 16 : (NR + 15) / 16 * 16;
   static constexpr int LO = NR;                               // first lo column (e4m3)
   static constexpr int CH = E4M3 ? D / 128 : D / 64;          // 128-byte chunks of a row
   static constexpr int PB = D / 128;                          // 128-dim blocks of the output
-  static constexpr int SLOT = KT * 128;
+  static constexpr int CHUNK = KT * 128;                      // bytes of a chunk of a tile
+  static constexpr int G = kTSlotBytes / CHUNK;               // chunks of a ring slot
+  static constexpr int NS = CH / G;                           // slots of a tile's keys (or values)
+  static constexpr int PER = CH / PB / G;                     // slots of a 128-dim block
   static constexpr int NQ = KT == 64 && NR <= 8 ? 8 : N;      // query rows with padding
   static constexpr int QROT = E4M3 ? 2 * NQ * 128 : 0;        // fp16 rows of the rotated dims
   static constexpr int QB = CH * NQ * 128 + QROT;
@@ -102,7 +109,8 @@ struct TileCfg {
   static constexpr int HEADER = (sizeof(TileHeader<SG, H>) + 1023) / 1024 * 1024;
   static constexpr int BUDGET = 232448 - 1024 - HEADER;
   static constexpr int COL_O = 2 * N;
-  static_assert(COL_O + PB * N <= 512, "TMEM columns");
+  static_assert(COL_O + TG * PB * N <= 512, "TMEM columns");
+  static_assert(CH % G == 0 && PER >= 1, "slots of a tile");
 };
 
 // Frequencies of the first 64 rotary pairs, theta_j / (2 pi), and the factor of 64 pairs on.
@@ -121,7 +129,7 @@ __host__ __device__ inline TileBufs tile_bufs(bool kv_same, bool rot) {
   // As much ring as three tiles, then a second buffer for the rotated copy, then one for the
   // next unit's query rows.
   TileBufs b;
-  const int tile = C::CH * C::SLOT * (kv_same ? 1 : 2);
+  const int tile = C::NS * kTSlotBytes * (kv_same ? 1 : 2);
   int left = C::BUDGET - C::QB - 2 * C::P_B - (rot ? C::ROT : 0);
   b.nq = b.nrot = 1;
   if (!rot) b.nrot = 0;
@@ -133,16 +141,18 @@ __host__ __device__ inline TileBufs tile_bufs(bool kv_same, bool rot) {
     b.nq = 2;
     left -= C::QB;
   }
-  int slots = left / C::SLOT;
+  int slots = left / kTSlotBytes;
   if (slots > kTMaxSlots) slots = kTMaxSlots;
   // the loads run at most four tiles ahead of the rotation (rot_in has four barriers)
-  if (rot && slots > 4 * C::CH) slots = 4 * C::CH;
+  if (rot && slots > 4 * C::NS) slots = 4 * C::NS;
+  // the slots of a block lie together
+  constexpr int even = ~(C::PER - 1);
   if (kv_same) {
-    b.kslots = slots & ~1;
+    b.kslots = slots & even;
     b.vslots = 0;
   } else {
-    b.kslots = (slots / 2) & ~1;
-    b.vslots = (slots - b.kslots) & ~1;
+    b.kslots = (slots / 2) & even;
+    b.vslots = (slots - b.kslots) & even;
   }
   return b;
 }
@@ -160,6 +170,13 @@ __device__ __forceinline__ int chunk_at(int i) {
   return 2 * block_at<PB>(i >> 1) + (i & 1);
 }
 
+__device__ __forceinline__ void tma_load_4d(void* smem, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+          smem_u32(smem)),
+      "l"(m), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
 __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -176,9 +193,6 @@ __host__ __device__ constexpr uint32_t idesc_zero_fmt(int M, int N, int a_mn, in
 __device__ __forceinline__ void tmem_ld_x4(uint32_t a, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
-}
-__device__ __forceinline__ void tmem_ld_x1(uint32_t a, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(a));
 }
 __device__ __forceinline__ void tmem_ld_x8(uint32_t a, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -323,6 +337,9 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
                   const __grid_constant__ PagedAttendArgs a, const __grid_constant__ TileTurns turns) {
   using C = TileCfg<D, E4M3, SG, H>;
   constexpr int KT = C::KT, N = C::N, NQ = C::NQ, NR = C::NR, CH = C::CH, PB = C::PB, HALF = D / 2;
+  constexpr int G = C::G, NS = C::NS, TG = C::TG;
+  // slot of a tile that holds the second half's rotated dims (the first holds the first half's)
+  constexpr int ROT2 = G == 2 ? 1 : E4M3 ? (PB > 1 ? 1 : 0) : (PB > 1 ? 2 : 1);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   using Header = TileHeader<SG, H>;
@@ -334,7 +351,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
   uint8_t* p_s = q_s + bufs.nq * C::QB;
   uint8_t* rot_s = p_s + 2 * C::P_B;
   uint8_t* kring = rot_s + bufs.nrot * C::ROT;
-  uint8_t* vring = kring + bufs.kslots * C::SLOT;
+  uint8_t* vring = kring + bufs.kslots * kTSlotBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -349,7 +366,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
       mbar_init(&hd->q_empty[i], 1);
       mbar_init(&hd->rot_ready[i], C::HW);
       mbar_init(&hd->s_full[i], 1);
-      mbar_init(&hd->p_full[i], 4 * SG);
+      mbar_init(&hd->p_full[i], 4 * SG);  // the groups that form a tile's weights
       mbar_init(&hd->pv_done[i], 1);
       mbar_init(&hd->hmeet[i], 4);
       mbar_init(&hd->mma_done[i], 1);
@@ -359,7 +376,8 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
       mbar_init(&hd->piece_full[i], 1);
       mbar_init(&hd->piece_empty[i], 15);  // every warp but the one that hands pieces out
     }
-    mbar_init(&hd->o_empty, 4 * SG);
+    mbar_init(&hd->o_empty, 8);
+    mbar_init(&hd->o_meet, 8);
     hd->abort_flag = 0;
     fence_barrier_init();
   }
@@ -404,91 +422,77 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
-    if (elect_one()) {
-      const int ps = 1 << a.c.page_shift, box = min(ps, KT), boxes = KT / box;
-      int ks = 0, vs = 0, t = 0;
-      uint32_t kph = 0, vph = 0, edge_ph = 0;    // edge_ph bit s: parity of slot s's next edge load
-      uint32_t last_full = 0, last_edge = 0;     // slots whose last load completes on full / edge
-      bool ok = true;
+    // The warp walks together, a lane per page box of a tile for what differs between boxes; one
+    // thread, by elect.sync, issues (copies issued by divergent lanes cost some 200 cycles each).
+    const int ps = 1 << a.c.page_shift, box = min(ps, KT), boxes = KT / box;
+    int ks = 0, vs = 0, t = 0;
+    uint32_t kph = 0, vph = 0, edge_ph = 0;    // edge_ph bit s: parity of slot s's next edge load
+    uint32_t last_full = 0, last_edge = 0;     // slots whose last load completes on full / edge
+    bool ok = true;
 #pragma unroll 1
-      for (int piece = 0; ok && piece_next(piece, p); ++piece) {
-        const int32_t* table = a.c.table + (size_t)p.b * a.c.max_blocks;
-        // Table entries of a tile's boxes, read a tile ahead; -1 for a box that no query sees
-        int next[8];
-        auto read_entries = [&](int kt) {
-#pragma unroll
-          for (int i = 0; i < KT / 16; ++i) {
-            const int pos = kt * KT + i * box;
-            next[i] = i < boxes && pos < p.end && pos + box > p.first ? __ldg(table + (pos >> a.c.page_shift)) : -1;
-          }
-        };
-        read_entries(p.kt0);
+    for (int piece = 0; ok && piece_at(piece, p); ++piece) {
+      const int32_t* table = a.c.table + (size_t)p.b * a.c.max_blocks;
+      // Whether some query sees this lane's box of tile kt, and its table entry, read a tile ahead
+      auto seen = [&](int kt) { return lane < boxes && kt * KT + lane * box < p.end && kt * KT + (lane + 1) * box > p.first; };
+      auto entry = [&](int kt) { return seen(kt) ? __ldg(table + ((kt * KT + lane * box) >> a.c.page_shift)) : -1; };
+      int next = entry(p.kt0);
 #pragma unroll 1
-        for (int lt = 0; lt < p.ntiles && ok; ++lt, ++t) {
-          const int kt = p.kt0 + lt, slot_row = (kt * KT) & (ps - 1);  // a box's rows follow the tile's first
-          int plane[8];
-          uint32_t count = 0;
-#pragma unroll
-          for (int i = 0; i < KT / 16; ++i) {
-            const int pos = kt * KT + i * box, e = next[i];
-            const bool used = i < boxes && pos < p.end && pos + box > p.first;
-            plane[i] = used ? e * a.c.hkv + p.kvh : -1;
-            if (used && (unsigned)e >= (unsigned)a.c.num_pages) {
-              atomicOr(&g_status, kStatusPage);
-              plane[i] = a.c.num_pages * a.c.hkv;  // past the pool: zeros
-            }
-            count += used;
-          }
-          if (lt + 1 < p.ntiles) read_entries(kt + 1);
-          const bool cut = kt * KT < p.first || (kt + 1) * KT > p.end;
-          // The tile's chunks, a block's (or two blocks') at a time: its slots are free first, then
-          // its boxes go out together, a row's columns one after the other.
+      for (int lt = 0; lt < p.ntiles && ok; ++lt, ++t) {
+        const int kt = p.kt0 + lt, row = boxes > 1 ? 0 : (kt * KT) & (ps - 1);
+        const bool used = seen(kt);
+        int plane = next * a.c.hkv + p.kvh;
+        if (used && (unsigned)next >= (unsigned)a.c.num_pages) {
+          atomicOr(&g_status, kStatusPage);
+          plane = a.c.num_pages * a.c.hkv;     // past the pool: zeros
+        }
+        const uint32_t mask = __ballot_sync(0xffffffffu, used);
+        const uint32_t bytes = (uint32_t)(__popc(mask) * box * 128 * G);
+        if (lt + 1 < p.ntiles) next = entry(kt + 1);
+        const bool cut = kt * KT < p.first || (kt + 1) * KT > p.end;
 #pragma unroll 1
-          for (int v = 0; v < (SAME ? 1 : 2) && ok; ++v) {
-            const CUtensorMap* map = v ? &v_map : &k_map;
-            uint8_t* ring = v ? vring : kring;
-            const int bar0 = v ? bufs.kslots : 0, slots = v ? bufs.vslots : bufs.kslots;
-            const bool clear = cut && (SAME || v);
-            int s = v ? vs : ks;
-            uint32_t f = v ? vph : kph;
-            uint64_t* bars = clear ? hd->edge : hd->full;
-            constexpr int G = CH >= 2 ? 2 : 1;  // chunks of a step: slot counts are even, a step does not wrap
+        for (int v = 0; v < (SAME ? 1 : 2) && ok; ++v) {
+          const CUtensorMap* map = v ? &v_map : &k_map;
+          uint8_t* ring = v ? vring : kring;
+          const int bar0 = v ? bufs.kslots : 0, slots = v ? bufs.vslots : bufs.kslots;
+          const bool clear = cut && (SAME || v);
+          uint64_t* bars = (clear ? hd->edge : hd->full) + bar0;
+          int s = v ? vs : ks;
+          uint32_t f = v ? vph : kph;
 #pragma unroll 1
-            for (int c0 = 0; c0 < CH && ok; c0 += G) {
-#pragma unroll
-              for (int j = 0; j < G; ++j) {
-                ok = ok && thread_wait(&hd->empty[bar0 + s + j], f ^ 1u, abort_flag);
-                const uint32_t bit = 1u << (bar0 + s + j);
-                last_edge = clear ? last_edge | bit : last_edge & ~bit;
-                last_full = clear ? last_full & ~bit : last_full | bit;
-                if (clear) edge_ph ^= bit;
-                if (ok) mbar_arrive_expect_tx(&bars[bar0 + s + j], count * box * 128);
-              }
-              if (!ok) break;
-#pragma unroll
-              for (int i = 0; i < KT / 16; ++i) {
-                if (plane[i] < 0) continue;
-#pragma unroll
-                for (int j = 0; j < G; ++j)
-                  tma_load_3d(ring + (s + j) * C::SLOT + i * box * 128, map, &bars[bar0 + s + j],
-                              chunk_at<PB, E4M3>(c0 + j) * (E4M3 ? 128 : 64), boxes > 1 ? 0 : slot_row, plane[i]);
-              }
-              if (rot && c0 <= (E4M3 ? 1 : 2) && c0 + G > (E4M3 ? (PB > 1 ? 1 : 0) : (PB > 1 ? 2 : 1)))
-                mbar_arrive(&hd->rot_in[t & 3]);  // the rotated chunks' loads have begun: their slots' barriers are in the phase to wait for
-              s += G;
-              if (s == slots) { s = 0; f ^= 1u; }
-            }
+          for (int i = 0; i < NS; ++i) {
+            ok = warp_wait(&hd->empty[bar0 + s], f ^ 1u, abort_flag);
             if (!ok) break;
-            if (v) {
-              vs = s;
-              vph = f;
-            } else {
-              ks = s;
-              kph = f;
+            const uint32_t bit = 1u << (bar0 + s);
+            last_edge = clear ? last_edge | bit : last_edge & ~bit;
+            last_full = clear ? last_full & ~bit : last_full | bit;
+            if (clear) edge_ph ^= bit;
+            uint64_t* bar = &bars[s];
+            uint8_t* dst = ring + s * kTSlotBytes;
+            const int c = chunk_at<PB, E4M3>(i * G);
+            if (elect_one()) mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll 1
+            for (uint32_t m = mask; m != 0; m &= m - 1) {
+              const int bx = __ffs(m) - 1, pl = __shfl_sync(0xffffffffu, plane, bx);
+              if (elect_one()) {
+                tma_load_4d(dst + bx * box * 128, map, bar, 0, row, c, pl);  // both chunks, if the box is the tile
+                if (G == 2 && boxes > 1) tma_load_4d(dst + C::CHUNK + bx * box * 128, map, bar, 0, row, c + 1, pl);
+              }
             }
+            // The rotated chunks' loads have begun: their slots' barriers are in the phase to wait for.
+            if (rot && i == ROT2 && lane == 0) mbar_arrive(&hd->rot_in[t & 3]);
+            if (++s == slots) { s = 0; f ^= 1u; }
+          }
+          if (v) {
+            vs = s;
+            vph = f;
+          } else {
+            ks = s;
+            kph = f;
           }
         }
       }
+    }
+    if (lane == 0) {
       // the last load of every slot lands before the CTA can leave (the barrier's phase parity: of a
       // plain load the one its slot's next fill would flip, of an edge load the last used)
 #pragma unroll 1
@@ -523,20 +527,17 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
           // S^T(t) overwrites the scores that softmax(t - 2) read
           if (t >= 2) ok = thread_wait(&hd->p_full[t & 1], (uint32_t)((t - 2) >> 1) & 1u, abort_flag);
           uint32_t acc = 0;
-          // first the chunks (their unrotated steps) as they land, two at a time so that the MMAs'
-          // operands are formed ahead of their issue; then the rotated copy
-          constexpr int G = CH >= 2 ? 2 : 1;
+          // first the chunks (their unrotated steps) as they land, then the rotated copy
 #pragma unroll 1
-          for (int i = 0; i < CH && ok; i += G) {
-#pragma unroll
-            for (int j = 0; j < G; ++j) ok = ok && thread_wait(&hd->full[ks + j], kph, abort_flag);
+          for (int i = 0; i < NS; ++i) {
+            ok = thread_wait(&hd->full[ks], kph, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t kd0 = sdesc_sw128(smem_u32(kring + ks * C::SLOT), 16, 1024);
+            const uint64_t kd0 = sdesc_sw128(smem_u32(kring + ks * kTSlotBytes), 16, 1024);
 #pragma unroll
             for (int j = 0; j < G; ++j) {
-              const int c = chunk_at<PB, E4M3>(i + j);
-              const uint64_t kd = kd0 + j * (C::SLOT >> 4);
+              const int c = chunk_at<PB, E4M3>(i * G) + j;
+              const uint64_t kd = kd0 + j * (C::CHUNK >> 4);
               const uint64_t qd = q_desc + (uint64_t)(c * (NQ * 8));
               if constexpr (E4M3) {
                 // the rotated dims are the first 64 of the row and of its second half
@@ -558,10 +559,9 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
                 umma_ss(sb, kd + 6, qd + 6, id16, 1);
                 acc = 1;
               }
-              if (!SAME) umma_commit(&hd->empty[ks + j]);
             }
-            ks += G;
-            if (ks == bufs.kslots) { ks = 0; kph ^= 1u; }
+            if (!SAME) umma_commit(&hd->empty[ks]);
+            if (++ks == bufs.kslots) { ks = 0; kph ^= 1u; }
           }
           if (ok && rot) {
             ok = thread_wait(&hd->rot_ready[t % bufs.nrot], (uint32_t)(t / bufs.nrot) & 1u, abort_flag);
@@ -570,7 +570,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               if (!ok) break;
-              const uint64_t kd = rd + i * (C::SLOT >> 4), qd = q_desc + (uint64_t)((E4M3 ? CH + i : i * (HALF / 64)) * (NQ * 8));
+              const uint64_t kd = rd + i * (C::CHUNK >> 4), qd = q_desc + (uint64_t)((E4M3 ? CH + i : i * (HALF / 64)) * (NQ * 8));
               umma_ss(sb, kd, qd, id16, acc);
               umma_ss(sb, kd + 2, qd + 2, id16, 1);
               umma_ss(sb, kd + 4, qd + 4, id16, 1);
@@ -607,24 +607,23 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
           const uint32_t p_addr = smem_u32(p_s + (t & 1) * C::P_B);
 #pragma unroll 1
           for (int i = 0; i < PB && ok; ++i) {
-            constexpr int per = CH / PB;  // chunks of a block
             if (!SAME)                    // K=V chunks have landed: the scores of this tile needed them
 #pragma unroll
-              for (int j = 0; j < per; ++j) ok = ok && thread_wait(&hd->full[bar0 + vs + j], vph, abort_flag);
+              for (int j = 0; j < C::PER; ++j) ok = ok && thread_wait(&hd->full[bar0 + vs + j], vph, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t vd = sdesc_sw128(smem_u32(ring + vs * C::SLOT), C::SLOT, 1024);
+            const uint64_t vd = sdesc_sw128(smem_u32(ring + vs * kTSlotBytes), C::CHUNK, 1024);
             const uint64_t pd = sdesc_sw128(p_addr, 16, 1024);
-            const uint32_t d = tmem + C::COL_O + (uint32_t)block_at<PB>(i) * N;
+            const uint32_t d = tmem + C::COL_O + (uint32_t)((TG == 2 ? (t & 1) * PB : 0) + block_at<PB>(i)) * N;
 #pragma unroll
             for (int kk = 0; kk < KT / (E4M3 ? 32 : 16); ++kk) {
-              const uint32_t acc = kk != 0 ? 1u : (uint32_t)(lt != 0);
+              const uint32_t acc = kk != 0 ? 1u : (uint32_t)(lt >= TG);
               if constexpr (E4M3) umma_f8(d, vd + 256 * kk, pd + 2 * kk, id, acc);
               else umma_ss(d, vd + 128 * kk, pd + (kk >> 2) * (N * 8) + 2 * (kk & 3), id, acc);
             }
 #pragma unroll
-            for (int j = 0; j < per; ++j) umma_commit(&hd->empty[bar0 + vs + j]);
-            vs += per;
+            for (int j = 0; j < C::PER; ++j) umma_commit(&hd->empty[bar0 + vs + j]);
+            vs += C::PER;
             if (vs == slots) { vs = 0; vph ^= 1u; }
           }
           if (!ok) break;
@@ -668,16 +667,19 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
         const int k0 = (p.kt0 + lt) * KT;
         const int lo = max(p.first - k0, 0), hi = min(p.end - k0, KT);
 #pragma unroll 1
-        for (int i = 0; i < CH && ok; ++i) {
+        for (int i = 0; i < NS && ok; ++i) {
           if (lo > 0 || hi < KT) {
             ok = warp_wait(&hd->edge[bar0 + s], (edge_ph >> s) & 1u, abort_flag);
             if (!ok) break;
             edge_ph ^= 1u << s;
-            uint4* rows = reinterpret_cast<uint4*>(ring + s * C::SLOT);
 #pragma unroll 1
-            for (int x = lane; x < lo * 8; x += 32) rows[x] = make_uint4(0u, 0u, 0u, 0u);
+            for (int j = 0; j < G; ++j) {
+              uint4* rows = reinterpret_cast<uint4*>(ring + s * kTSlotBytes + j * C::CHUNK);
 #pragma unroll 1
-            for (int x = hi * 8 + lane; x < KT * 8; x += 32) rows[x] = make_uint4(0u, 0u, 0u, 0u);
+              for (int x = lane; x < lo * 8; x += 32) rows[x] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+              for (int x = hi * 8 + lane; x < KT * 8; x += 32) rows[x] = make_uint4(0u, 0u, 0u, 0u);
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&hd->full[bar0 + s]);
@@ -701,8 +703,11 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
         return false;
       uint8_t* qd = q_s + qb * C::QB;
       constexpr int QI = (HALF + 63) / 64;   // words of two pairs per lane and half row
+      constexpr int RW = NR / C::HW;         // rows of a warp, one after the other: they share tokens, and angles
+      int angle_tk = -1;
+      float2 c0[QI], c1[QI];
 #pragma unroll 1
-      for (int row = hw; row < NR; row += C::HW) {
+      for (int row = hw * RW; row < (hw + 1) * RW; ++row) {
         const bool have = row < np.rows;
         const int tk = (np.row0 + row) / a.group, hh = np.row0 + row - tk * a.group;
         const int orow = (np.tok0 + tk) * a.hq + np.kvh * a.group + hh;
@@ -711,53 +716,60 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
           hd->orow[q_piece & 3][row] = orow;
           hd->qpos[q_piece & 3][row] = np.len + tk;
         }
-        // e4m3 goes over the row twice: for its largest magnitude, then to scale and split it
-        uint32_t top = 0;
-        float up = 1.f;
-#pragma unroll 1
-        for (int i = 0; i < (E4M3 ? 2 : 1) * QI; ++i) {
-          const bool store = !E4M3 || i >= QI;
-          if (E4M3 && i == QI) {
+        uint32_t w0[QI], w1[QI];
 #pragma unroll
-            for (int m = 16; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-            // the largest magnitude is in [2^(E - 127), 2^(E - 126)): to [2^7, 2^8) by 2^(134 - E). A
-            // NaN or an infinity must reach the row's scores, and goes into the row's factor.
-            const int E = (int)(top >> 23);
-            const int k = top == 0u || E == 255 ? 0 : min(max(134 - E, -126), 126);
-            up = __uint_as_float((uint32_t)(127 + k) << 23);
-            if (lane == 0)
-              hd->qsc[q_piece & 3][row] =
-                  E == 255 ? __uint_as_float(0x7FC00000u)
-                           : a.softmax_scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 - k) << 23);
-          }
-          const int far = i % QI, j = 2 * lane + 64 * far;
-          if (j >= HALF) continue;
-          uint32_t w0 = 0u, w1 = 0u;
-          if (have) {
-            w0 = __ldg(reinterpret_cast<const uint32_t*>(src + j));
-            w1 = __ldg(reinterpret_cast<const uint32_t*>(src + HALF + j));
-          }
-          float x00 = __uint_as_float(w0 << 16), x01 = __uint_as_float(w0 & 0xFFFF0000u);
-          float x10 = __uint_as_float(w1 << 16), x11 = __uint_as_float(w1 & 0xFFFF0000u);
-          if (j < a.r) {
-            double f0 = turns.freq[2 * lane], f1 = turns.freq[2 * lane + 1];  // `far` times 64 pairs on
-#pragma unroll 1
-            for (int k = 0; k < far; ++k) {
+        for (int i = 0; i < QI; ++i) {
+          const bool get = have && 2 * lane + 64 * i < HALF;
+          w0[i] = get ? __ldg(reinterpret_cast<const uint32_t*>(src + 2 * lane + 64 * i)) : 0u;
+          w1[i] = get ? __ldg(reinterpret_cast<const uint32_t*>(src + HALF + 2 * lane + 64 * i)) : 0u;
+        }
+        if (have && tk != angle_tk) {
+          angle_tk = tk;
+          double f0 = turns.freq[2 * lane], f1 = turns.freq[2 * lane + 1];  // 64 pairs on each time
+#pragma unroll
+          for (int i = 0; i < QI; ++i) {
+            const int j = 2 * lane + 64 * i;
+            c0[i] = c1[i] = make_float2(1.f, 0.f);
+            if (64 * i < a.r) {
+              if (j < a.r) c0[i] = turn_of((double)(np.len + tk), f0);
+              if (j + 1 < a.r) c1[i] = turn_of((double)(np.len + tk), f1);
               f0 *= turns.step64;
               f1 *= turns.step64;
             }
-            const float2 c0 = turn_of((double)(np.len + tk), f0), c1 = turn_of((double)(np.len + tk), j + 1 < a.r ? f1 : 0.0);
-            w0 = pack_bf16x2(x00 * c0.x - x10 * c0.y, x01 * c1.x - x11 * c1.y);
-            w1 = pack_bf16x2(x00 * c0.y + x10 * c0.x, x01 * c1.y + x11 * c1.x);
           }
-          if (!store) {
-            top = max(max(top, max((w0 & 0x7FFFu) << 16, w0 & 0x7FFF0000u)), max((w1 & 0x7FFFu) << 16, w1 & 0x7FFF0000u));
-            continue;
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < QI; ++i) {
+          if (have && 64 * i < a.r) {
+            const float x00 = __uint_as_float(w0[i] << 16), x01 = __uint_as_float(w0[i] & 0xFFFF0000u);
+            const float x10 = __uint_as_float(w1[i] << 16), x11 = __uint_as_float(w1[i] & 0xFFFF0000u);
+            w0[i] = pack_bf16x2(x00 * c0[i].x - x10 * c0[i].y, x01 * c1[i].x - x11 * c1[i].y);
+            w1[i] = pack_bf16x2(x00 * c0[i].y + x10 * c0[i].x, x01 * c1[i].y + x11 * c1[i].x);
           }
-#pragma unroll 1
+          if (E4M3) top = max(max(top, max((w0[i] & 0x7FFFu) << 16, w0[i] & 0x7FFF0000u)), max((w1[i] & 0x7FFFu) << 16, w1[i] & 0x7FFF0000u));
+        }
+        float up = 1.f;
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int m = 16; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+          // the largest magnitude is in [2^(E - 127), 2^(E - 126)): to [2^7, 2^8) by 2^(134 - E). A
+          // NaN or an infinity must reach the row's scores, and goes into the row's factor.
+          const int E = (int)(top >> 23);
+          const int k = top == 0u || E == 255 ? 0 : min(max(134 - E, -126), 126);
+          up = __uint_as_float((uint32_t)(127 + k) << 23);
+          if (lane == 0)
+            hd->qsc[q_piece & 3][row] =
+                E == 255 ? __uint_as_float(0x7FC00000u)
+                         : a.softmax_scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 - k) << 23);
+        }
+#pragma unroll
+        for (int i = 0; i < QI; ++i) {
+          if (2 * lane + 64 * i >= HALF) continue;
+#pragma unroll
           for (int part = 0; part < 2; ++part) {
-            const int dim = part * HALF + j;
-            const uint32_t w = part ? w1 : w0;
+            const int dim = part * HALF + 64 * i + 2 * lane;
+            const uint32_t w = part ? w1[i] : w0[i];
             if constexpr (!E4M3) {
               *reinterpret_cast<uint32_t*>(qd + (dim >> 6) * NQ * 128 + sw128(row, (dim & 63) * 2)) = w;
             } else {
@@ -767,7 +779,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
               uint8_t* chunk = qd + (dim >> 7) * NQ * 128;
               *reinterpret_cast<uint16_t*>(chunk + sw128(row, dim & 127)) = (uint16_t)hi;
               *reinterpret_cast<uint16_t*>(chunk + sw128(C::LO + row, dim & 127)) = (uint16_t)e4m3x2(x0 - h.x, x1 - h.y);
-              if (j < 64) *reinterpret_cast<uint32_t*>(qd + (CH + part) * NQ * 128 + sw128(row, j * 2)) = pack_f16x2(x0, x1);
+              if (i == 0) *reinterpret_cast<uint32_t*>(qd + (CH + part) * NQ * 128 + sw128(row, 4 * lane)) = pack_f16x2(x0, x1);
             }
           }
         }
@@ -817,8 +829,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
           }
           // the slots of the two rotated chunks, whose loads have begun (so that their barriers'
           // phases are the ones to wait for), and the copy's buffer, whose last scores are done
-          const int i1 = E4M3 ? (PB > 1 ? 1 : 0) : (PB > 1 ? 2 : 1);
-          int s1 = ks + i1;
+          int s1 = ks + ROT2;
           const bool wrap = s1 >= bufs.kslots;
           if (wrap) s1 -= bufs.kslots;
           ok = warp_wait(&hd->rot_in[t & 3], (uint32_t)(t >> 2) & 1u, abort_flag);
@@ -827,8 +838,8 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
           if (ok) ok = warp_wait(&hd->full[ks], kph, abort_flag);
           if (ok) ok = warp_wait(&hd->full[s1], wrap ? kph ^ 1u : kph, abort_flag);
           if (!ok) break;
-          const uint8_t* c0 = kring + ks * C::SLOT;
-          const uint8_t* c1 = kring + s1 * C::SLOT;
+          const uint8_t* c0 = kring + ks * kTSlotBytes;
+          const uint8_t* c1 = kring + s1 * kTSlotBytes;
           uint8_t* dst = rot_s + (t % bufs.nrot) * C::ROT;
           float bc[4], bs[4];
 #pragma unroll
@@ -864,7 +875,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
             const uint32_t off = sw128(row, 8 * ku);
             *reinterpret_cast<uint2*>(dst + off) =
                 E4M3 ? make_uint2(pack_f16x2(y0[0], y0[1]), pack_f16x2(y0[2], y0[3])) : make_uint2(pack_bf16x2(y0[0], y0[1]), pack_bf16x2(y0[2], y0[3]));
-            *reinterpret_cast<uint2*>(dst + C::SLOT + off) =
+            *reinterpret_cast<uint2*>(dst + C::CHUNK + off) =
                 E4M3 ? make_uint2(pack_f16x2(y1[0], y1[1]), pack_f16x2(y1[2], y1[3])) : make_uint2(pack_bf16x2(y1[0], y1[1]), pack_bf16x2(y1[2], y1[3]));
           }
           fence_proxy_async_smem();
@@ -876,7 +887,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
             as[e] = ac[e] * ts[e] + as[e] * tc[e];
             ac[e] = nc;
           }
-          ks += CH;
+          ks += NS;
           if (ks >= bufs.kslots) { ks -= bufs.kslots; kph ^= 1u; }
         }
       }
@@ -885,7 +896,9 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
   } else {
     // ------------------------------------------------------------ softmax and output
     const int quad = warp & 3, half = (warp - 4 - C::HW) >> 2;
-    const uint32_t lane_tmem = tmem + ((uint32_t)(quad * 32) << 16) + half * H;
+    const int rh = SG == 2 ? half * H : 0;                    // first row of this group
+    const uint32_t lane_tmem = tmem + ((uint32_t)(quad * 32) << 16) + rh;
+    const uint32_t my_o = lane_tmem + C::COL_O + (TG == 2 ? half * PB * N : 0);
     const bool key_lane = KT == 128 || lane < 16;             // TMEM lanes of M = 64: 16 per quadrant
     const int u = KT == 128 ? quad * 32 + lane : quad * 16 + (lane & 15);
     // Headroom over the running references: weights of up to 2^8, in e4m3 up to 2^8.75 < 448 (its
@@ -895,10 +908,10 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
     uint32_t col[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int cb = E4M3 ? u : (u & 63) * 2, r7 = (j + half * H) & 7;
+      const int cb = E4M3 ? u : (u & 63) * 2, r7 = (j + rh) & 7;
       col[j] = (((cb >> 4) ^ r7) << 4) | (cb & 15);
     }
-    const uint32_t p_mine = smem_u32(p_s) + half * H * 128 + (E4M3 ? 0 : (u >> 6) * N * 128);
+    const uint32_t p_mine = smem_u32(p_s) + rh * 128 + (E4M3 ? 0 : (u >> 6) * N * 128);
     uint32_t meets = 0;
     bool ok = true;
     auto meet = [&]() {
@@ -907,9 +920,10 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
       ok = warp_wait(&hd->hmeet[half], meets & 1u, abort_flag);
       ++meets;
     };
-    int t = 0;
+    int t0 = 0;                            // tiles of the units before
 #pragma unroll 1
     for (int piece = 0; ok && piece_at(piece, p); ++piece) {
+      const int lt0 = TG == 2 ? (half ^ t0) & 1 : 0;  // this group's first tile; then every TG-th
       // m: reference of the sums; mv: of the weights (bf16: the same one). A row that has seen no key
       // has the lowest finite number.
       float m_run[H], mv_run[E4M3 ? H : 1], l_acc[H];
@@ -926,7 +940,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
       // them two tiles ahead, so that no tile waits for either
       float ks_next = 1.f, vs_next = 1.f;
       int entry = -1;
-      auto read_ahead = [&](int lt) {  // scales of tile lt, entry of tile lt + 1
+      auto read_ahead = [&](int lt) {  // scales of tile lt, entry of the group's next
         const int pos = (p.kt0 + lt) * KT + u, ps = a.c.page_shift;
         ks_next = vs_next = 1.f;
         if ((unsigned)entry < (unsigned)a.c.num_pages) {
@@ -934,19 +948,19 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
           ks_next = __ldg(a.c.k_scales + row);
           if (!SAME) vs_next = __ldg(a.c.v_scales + row);
         }
-        const int np = pos + KT;
-        entry = lt + 1 < p.ntiles && np >= p.first && np < p.end ? __ldg(a.c.table + (size_t)p.b * a.c.max_blocks + (np >> ps)) : -1;
+        const int np = pos + TG * KT;
+        entry = lt + TG < p.ntiles && np >= p.first && np < p.end ? __ldg(a.c.table + (size_t)p.b * a.c.max_blocks + (np >> ps)) : -1;
       };
 #pragma unroll 1
-      for (int lt = E4M3 ? -2 : 0; lt < p.ntiles && ok; ++lt) {
+      for (int lt = E4M3 ? lt0 - 2 * TG : lt0; lt < p.ntiles && ok; lt += TG) {
         float kscale = 1.f, vscale = 1.f;
         if constexpr (E4M3) {
           kscale = ks_next;
           vscale = SAME ? ks_next : vs_next;
-          read_ahead(lt + 1);
+          read_ahead(lt + TG);
           if (lt < 0) continue;
         }
-        const int bb = t & 1, k0 = (p.kt0 + lt) * KT;
+        const int t = t0 + lt, bb = t & 1, k0 = (p.kt0 + lt) * KT;
         ok = warp_wait(&hd->s_full[bb], (uint32_t)(t >> 1) & 1u, abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -958,7 +972,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
           float s2[H];
           tmem_ld_n<H>(lane_tmem + bb * N + C::LO, reinterpret_cast<uint32_t*>(s2));
           tmem_ld_wait();
-          const float* cf = &hd->qsc[piece & 3][half * H];
+          const float* cf = &hd->qsc[piece & 3][rh];
 #pragma unroll
           for (int q = 0; q < H; ++q) sv[q] = (sv[q] + s2[q]) * (cf[q] * kscale);
         } else {
@@ -972,7 +986,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
           const int pos = key_lane ? k0 + u : 0x7fffffff;
 #pragma unroll
           for (int q = 0; q < H; ++q) {
-            const int qp = hd->qpos[piece & 3][half * H + q];
+            const int qp = hd->qpos[piece & 3][rh + q];
             if (pos > qp || (a.is_local && pos <= qp - a.window)) sv[q] = -INFINITY;
           }
         }
@@ -1034,18 +1048,16 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
             l_acc[q] *= hd->step[half][0][q];
             al[q] = hd->step[half][1][q];
           }
-          // O^T is touched once the products of the tile before are done (a unit's first tile has
-          // nothing to rescale)
-          if (lt >= 1) {
-            ok = warp_wait(&hd->pv_done[bb ^ 1], (uint32_t)((t - 1) >> 1) & 1u, abort_flag);
+          // The group's output is touched once the products of its tile before are done (its first
+          // tile in a unit has nothing to rescale).
+          if (lt >= TG) {
+            ok = warp_wait(&hd->pv_done[(t - TG) & 1], (uint32_t)((t - TG) >> 1) & 1u, abort_flag);
             if (!ok) break;
             tc_fence_after();
-          }
-          if (lt >= 1) {
 #pragma unroll 1
             for (int i = 0; i < PB * (E4M3 ? 2 : 1); ++i) {
               uint32_t o[H];
-              const uint32_t ta = lane_tmem + C::COL_O + (uint32_t)((i % PB) * N + (i / PB) * C::LO);
+              const uint32_t ta = my_o + (uint32_t)((i % PB) * N + (i / PB) * C::LO);
               tmem_ld_n<H>(ta, o);
               tmem_ld_wait();
 #pragma unroll
@@ -1088,7 +1100,6 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&hd->p_full[bb]);
-        ++t;
       }
       if (!ok) break;
       // ---- the unit's (or its part's) output. The rows' sums: halves of the values go to the lanes of
@@ -1099,46 +1110,86 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
 #pragma unroll
         for (int q = 0; q < HP; ++q) x[q] = q < H ? l_acc[q] : 0.f;
         const int mine = scatter_sums<16, HP / 2>(x, lane);  // the row this lane ends up with
-        auto& red = hd->red[meets & 1u][half];
-        if ((lane & (32 / HP - 1)) == 0) red[0][quad][mine] = x[0];
+        if ((lane & (32 / HP - 1)) == 0) hd->sums[piece & 1][half][quad][mine] = x[0];
         meet();
         if (!ok) break;
       }
-      ok = warp_wait(&hd->pv_done[(t - 1) & 1], (uint32_t)((t - 1) >> 1) & 1u, abort_flag);
+      // The groups that share the rows meet: their sums and references are there to read.
+      if (TG == 2) {
+        if (lane == 0) mbar_arrive(&hd->o_meet);
+        ok = warp_wait(&hd->o_meet, (uint32_t)piece & 1u, abort_flag);
+        if (!ok) break;
+      }
+      t0 += p.ntiles;
+      for (int i = 1; i <= min(TG, p.ntiles) && ok; ++i)
+        ok = warp_wait(&hd->pv_done[(t0 - i) & 1], (uint32_t)((t0 - i) >> 1) & 1u, abort_flag);
       if (!ok) break;
       tc_fence_after();
-      // lane q forms row q's factor, log-sum-exp and place
-      float fac_lane = 0.f;
+      // lane q forms row q's factors (of either group's output), log-sum-exp and place
+      float fac[TG] = {};
       int place = -1;
-      if (lane < H && half * H + lane < p.rows) {
-        const auto& red = hd->red[(meets - 1) & 1u][half];
-        const float l = (red[0][0][lane] + red[0][1][lane]) + (red[0][2][lane] + red[0][3][lane]), m = hd->refs[piece & 1][half][0][lane], mv = hd->refs[piece & 1][half][1][lane];
-        const int row = half * H + lane;
+      if (lane < H && rh + lane < p.rows) {
+        float l[TG], m[TG], mv[TG], top = -3.0e38f, sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < TG; ++g) {
+          const int gi = TG == 2 ? g : half;
+          const float* x = &hd->sums[piece & 1][gi][0][lane];
+          constexpr int Q = H <= 8 ? 8 : 32;
+          l[g] = (x[0] + x[Q]) + (x[2 * Q] + x[3 * Q]);
+          m[g] = fmaxf(hd->refs[piece & 1][gi][0][lane], -3.0e38f);
+          mv[g] = fmaxf(hd->refs[piece & 1][gi][1][lane], -3.0e38f);
+          top = fmaxf(top, m[g]);
+        }
+#pragma unroll
+        for (int g = 0; g < TG; ++g) {
+          fac[g] = fast_exp2(m[g] - top);
+          sum += l[g] * fac[g];
+        }
+        const int row = rh + lane;
         place = p.slot >= 0 ? p.slot * NR + row : hd->orow[piece & 3][row];
-        fac_lane = l > 0.f ? __fdividef(1.f, l) : l == 0.f ? 0.f : l;  // a NaN sum stays one
-        if (E4M3) fac_lane *= fast_exp2(fmaxf(mv, -3.0e38f) - fmaxf(m, -3.0e38f));
-        if (quad == 0) {
-          const float lse = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : l == 0.f ? -INFINITY : l;
+        const float inv = sum > 0.f ? __fdividef(1.f, sum) : sum == 0.f ? 0.f : sum;  // a NaN sum stays one
+#pragma unroll
+        for (int g = 0; g < TG; ++g) {
+          fac[g] *= inv;
+          if (E4M3) fac[g] *= fast_exp2(mv[g] - m[g]);
+        }
+        if (quad == 0 && (TG == 1 || half == 0)) {
+          const float lse = sum > 0.f ? (top + __log2f(sum)) * 0.6931471805599453f : sum == 0.f ? -INFINITY : sum;
           if (p.slot >= 0) a.partial_lse[place] = lse;
           else if (a.lse) a.lse[place] = lse;
         }
       }
       const bool wide = p.slot >= 0 || a.out_f32;
       uint8_t* out = p.slot >= 0 ? reinterpret_cast<uint8_t*>(a.partial_o) : static_cast<uint8_t*>(a.out);
-      // a row and a block of 128 dims at a time: 32 dims a warp
+      // A block of 128 dims at a time, 32 dims a warp; groups that share the rows take turns. With
+      // one tile only its group has an output.
+      const int gone = TG == 2 && p.ntiles == 1 ? (t0 & 1) : -1;
 #pragma unroll 1
-      for (int i = 0; i < PB * H; ++i) {
-        const int m = i / H, q = i - m * H, pl = __shfl_sync(0xffffffffu, place, q);
-        if (pl >= 0) {
-          uint32_t o[2];
-          tmem_ld_x1(lane_tmem + C::COL_O + (uint32_t)(m * N + q), o);
-          if constexpr (E4M3) tmem_ld_x1(lane_tmem + C::COL_O + (uint32_t)(m * N + C::LO + q), o + 1);
+      for (int m = TG == 2 ? half : 0; m < PB; m += TG) {
+        float v[H];
+#pragma unroll
+        for (int q = 0; q < H; ++q) v[q] = 0.f;
+#pragma unroll
+        for (int g = 0; g < TG; ++g) {
+          if (g == gone) continue;
+          const uint32_t ta = lane_tmem + C::COL_O + (uint32_t)((g * PB + m) * N);
+          uint32_t o[H], o2[H];
+          tmem_ld_n<H>(ta, o);
+          if constexpr (E4M3) tmem_ld_n<H>(ta + C::LO, o2);
           tmem_ld_wait();
-          const float sum = E4M3 ? __uint_as_float(o[0]) + __uint_as_float(o[1]) : __uint_as_float(o[0]);
-          const float v = sum * __shfl_sync(0xffffffffu, fac_lane, q);
-          const size_t at = (size_t)pl * D + m * 128 + quad * 32 + lane;
-          if (wide) reinterpret_cast<float*>(out)[at] = v;
-          else reinterpret_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+#pragma unroll
+          for (int q = 0; q < H; ++q) {
+            const float x = E4M3 ? __uint_as_float(o[q]) + __uint_as_float(o2[q]) : __uint_as_float(o[q]);
+            v[q] += x * __shfl_sync(0xffffffffu, fac[g], q);
+          }
+        }
+        const size_t col = m * 128 + quad * 32 + lane;
+#pragma unroll
+        for (int q = 0; q < H; ++q) {
+          const int pl = __shfl_sync(0xffffffffu, place, q);
+          if (pl < 0) continue;
+          if (wide) reinterpret_cast<float*>(out)[(size_t)pl * D + col] = v[q];
+          else reinterpret_cast<__nv_bfloat16*>(out)[(size_t)pl * D + col] = __float2bfloat16_rn(v[q]);
         }
       }
       // O^T has been read: the next unit's first products may overwrite it
@@ -1157,16 +1208,16 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
   }
 }
 
-// 3-D map over a page pool's byte rows or bf16 rows, 128-byte wide boxes of `rows` rows.
-static bool tile_map(CUtensorMap* m, const void* base, const PagedCache& c, bool e4m3, int rows) {
+// 4-D map over a page pool's rows as 128-byte column chunks: boxes of `rows` rows of `chunks` chunks.
+static bool tile_map(CUtensorMap* m, const void* base, const PagedCache& c, bool e4m3, int rows, int chunks) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const int esz = e4m3 ? 1 : 2, ps = 1 << c.page_shift;
-  cuuint64_t dims[3] = {(cuuint64_t)c.d, (cuuint64_t)ps, (cuuint64_t)c.num_pages * c.hkv};
-  cuuint64_t strides[2] = {(cuuint64_t)c.d * esz, (cuuint64_t)c.d * ps * esz};
-  cuuint32_t box[3] = {(cuuint32_t)(128 / esz), (cuuint32_t)rows, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+  cuuint64_t dims[4] = {(cuuint64_t)(128 / esz), (cuuint64_t)ps, (cuuint64_t)(c.d * esz / 128), (cuuint64_t)c.num_pages * c.hkv};
+  cuuint64_t strides[3] = {(cuuint64_t)c.d * esz, 128, (cuuint64_t)c.d * ps * esz};
+  cuuint32_t box[4] = {(cuuint32_t)(128 / esz), (cuuint32_t)rows, (cuuint32_t)chunks, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1189,15 +1240,15 @@ template <int D, bool E4M3, bool SAME, int SG, int H>
 static cudaError_t launch_tile_t(PagedAttendArgs a, bool cut, long long units, cudaStream_t stream) {
   using C = TileCfg<D, E4M3, SG, H>;
   const TileBufs b = tile_bufs<D, E4M3, SG, H>(SAME, SAME && a.r > 0);
-  if (b.kslots < C::CH || (!SAME && b.vslots < C::CH)) return cudaErrorInvalidValue;
+  if (b.kslots < C::NS || (!SAME && b.vslots < C::NS)) return cudaErrorInvalidValue;
   static std::atomic<bool> ready[64];
   cudaError_t e = allow_smem(paged_tile_kernel<D, E4M3, SAME, SG, H>, 232448, ready);
   if (e != cudaSuccess) return e;
-  const int box = std::min(1 << a.c.page_shift, C::KT);
+  const int box = std::min(1 << a.c.page_shift, C::KT), chunks = box == C::KT ? C::G : 1;
   CUtensorMap k, v;
-  if (!tile_map(&k, a.c.k, a.c, E4M3, box)) return cudaErrorInvalidValue;
+  if (!tile_map(&k, a.c.k, a.c, E4M3, box, chunks)) return cudaErrorInvalidValue;
   v = k;
-  if (!SAME && !tile_map(&v, a.c.v, a.c, E4M3, box)) return cudaErrorInvalidValue;
+  if (!SAME && !tile_map(&v, a.c.v, a.c, E4M3, box, chunks)) return cudaErrorInvalidValue;
   const int grid = cut ? kSms : (int)std::min<long long>(units, kSms);
   a.cut = cut;
   a.teams = grid;
