@@ -227,13 +227,12 @@ __device__ __forceinline__ void tmem_st_n(uint32_t a, const uint32_t* r) {
   }
 }
 
-// A bounded wait. Out of line, as is all that need not be in a role's loop: a CTA runs six
-// different loops, and where their code together does not stay in the SM's instruction caches
-// every tile fetches it again (measured on the 64-key K=V form: 85 KB of code 6,400 cycles a
-// tile, 78 KB 4,050). Each try suspends the warp for a while, so the limit on tries is seconds;
-// running out of them records a timeout.
-__device__ __noinline__ bool thread_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  bool ok = mbar_try_wait(bar, parity);
+// A bounded wait. The first try is in line (a role alone on its scheduler pays five cycles and
+// more for every instruction, and the barrier is mostly in the phase already); what follows is a
+// call, so that the six loops of a CTA stay small together. Each try suspends the warp for a
+// while, so the limit on tries is seconds; running out of them records a timeout.
+__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  bool ok = false;
 #pragma unroll 1
   for (int n = 0; !ok && !*abort; ++n) {
     ok = mbar_try_wait(bar, parity);
@@ -244,9 +243,13 @@ __device__ __noinline__ bool thread_wait(uint64_t* bar, uint32_t parity, volatil
   }
   return ok;
 }
+__device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_try_wait(bar, parity) || wait_more(bar, parity, abort);
+}
 // The same by a whole warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, thread_wait(bar, parity, abort));
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_more(bar, parity, abort));
 }
 
 __device__ __noinline__ float2 turn_of(double pos, double inv_freq_turns) {
@@ -457,15 +460,12 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
           const bool clear = cut && (SAME || v);
           uint64_t* bars = (clear ? hd->edge : hd->full) + bar0;
           int s = v ? vs : ks;
-          uint32_t f = v ? vph : kph;
+          uint32_t f = v ? vph : kph, filled = 0;
 #pragma unroll 1
           for (int i = 0; i < NS; ++i) {
             ok = warp_wait(&hd->empty[bar0 + s], f ^ 1u, abort_flag);
             if (!ok) break;
-            const uint32_t bit = 1u << (bar0 + s);
-            last_edge = clear ? last_edge | bit : last_edge & ~bit;
-            last_full = clear ? last_full & ~bit : last_full | bit;
-            if (clear) edge_ph ^= bit;
+            filled |= 1u << s;
             uint64_t* bar = &bars[s];
             uint8_t* dst = ring + s * kTSlotBytes;
             const int c = chunk_at<PB, E4M3>(i * G);
@@ -482,6 +482,10 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
             if (rot && i == ROT2 && lane == 0) mbar_arrive(&hd->rot_in[t & 3]);
             if (++s == slots) { s = 0; f ^= 1u; }
           }
+          filled <<= bar0;
+          last_edge = clear ? last_edge | filled : last_edge & ~filled;
+          last_full = clear ? last_full & ~filled : last_full | filled;
+          if (clear) edge_ph ^= filled;
           if (v) {
             vs = s;
             vph = f;
@@ -513,6 +517,9 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
     if (elect_one()) {
       const uint32_t id16 = E4M3 ? idesc_zero_fmt(KT, NQ, 0, 0) : umma_idesc_bf16(KT, NQ, 0, 0);
       const uint32_t id8 = idesc_zero_fmt(KT, NQ, 0, 0);
+      // descriptor of the K-major operand at 16-byte unit `at` of shared memory
+      const uint64_t desc0 = sdesc_sw128(0, 16, 1024);
+      auto desc_at = [&](uint32_t at) { return desc0 + at; };
       int ks = 0, t = 0;
       uint32_t kph = 0;
       bool ok = true;
@@ -520,25 +527,33 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
       for (int piece = 0; ok && piece_next(piece, p); ++piece) {
         const int qb = piece % bufs.nq;
         ok = thread_wait(&hd->q_full[qb], (uint32_t)(piece / bufs.nq) & 1u, abort_flag);
-        const uint64_t q_desc = sdesc_sw128(smem_u32(q_s + qb * C::QB), 16, 1024);
+        const uint32_t q_addr = smem_u32(q_s + qb * C::QB) >> 4, ring_addr = smem_u32(kring) >> 4;
 #pragma unroll 1
         for (int lt = 0; lt < p.ntiles && ok; ++lt, ++t) {
           const uint32_t sb = tmem + (uint32_t)(t & 1) * N;
           // S^T(t) overwrites the scores that softmax(t - 2) read
           if (t >= 2) ok = thread_wait(&hd->p_full[t & 1], (uint32_t)((t - 2) >> 1) & 1u, abort_flag);
           uint32_t acc = 0;
-          // first the chunks (their unrotated steps) as they land, then the rotated copy
-#pragma unroll 1
+          const int ks0 = ks;
+          // First the chunks' unrotated steps, then the rotated copy. The waits come before the MMAs
+          // (which the ring's depth allows: the loads are tiles ahead) so that the MMAs issue back to
+          // back, all descriptors one addition off a slot's.
+          uint32_t at[NS];
+#pragma unroll
           for (int i = 0; i < NS; ++i) {
-            ok = thread_wait(&hd->full[ks], kph, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t kd0 = sdesc_sw128(smem_u32(kring + ks * kTSlotBytes), 16, 1024);
+            ok = ok && thread_wait(&hd->full[ks], kph, abort_flag);
+            at[i] = ring_addr + (uint32_t)ks * (kTSlotBytes >> 4);
+            if (++ks == bufs.kslots) { ks = 0; kph ^= 1u; }
+          }
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
 #pragma unroll
             for (int j = 0; j < G; ++j) {
               const int c = chunk_at<PB, E4M3>(i * G) + j;
-              const uint64_t kd = kd0 + j * (C::CHUNK >> 4);
-              const uint64_t qd = q_desc + (uint64_t)(c * (NQ * 8));
+              const uint64_t kd = desc_at(at[i] + j * (C::CHUNK >> 4));
+              const uint64_t qd = desc_at(q_addr + (uint32_t)(c * (NQ * 8)));
               if constexpr (E4M3) {
                 // the rotated dims are the first 64 of the row and of its second half
                 const bool first = rot && (c * 128 == 0 || c * 128 == HALF), second = rot && HALF == 64;
@@ -560,17 +575,20 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
                 acc = 1;
               }
             }
-            if (!SAME) umma_commit(&hd->empty[ks]);
-            if (++ks == bufs.kslots) { ks = 0; kph ^= 1u; }
+            if (!SAME) {
+              int slot = ks0 + i;
+              if (slot >= bufs.kslots) slot -= bufs.kslots;
+              umma_commit(&hd->empty[slot]);
+            }
           }
           if (ok && rot) {
             ok = thread_wait(&hd->rot_ready[t % bufs.nrot], (uint32_t)(t / bufs.nrot) & 1u, abort_flag);
             tc_fence_after();
-            const uint64_t rd = sdesc_sw128(smem_u32(rot_s + (t % bufs.nrot) * C::ROT), 16, 1024);
+            const uint32_t rot_addr = smem_u32(rot_s + (t % bufs.nrot) * C::ROT) >> 4;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               if (!ok) break;
-              const uint64_t kd = rd + i * (C::CHUNK >> 4), qd = q_desc + (uint64_t)((E4M3 ? CH + i : i * (HALF / 64)) * (NQ * 8));
+              const uint64_t kd = desc_at(rot_addr + i * (C::CHUNK >> 4)), qd = desc_at(q_addr + (uint32_t)((E4M3 ? CH + i : i * (HALF / 64)) * (NQ * 8)));
               umma_ss(sb, kd, qd, id16, acc);
               umma_ss(sb, kd + 2, qd + 2, id16, 1);
               umma_ss(sb, kd + 4, qd + 4, id16, 1);
@@ -605,15 +623,23 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
           // a unit's first products overwrite the output that the last unit's epilogue has read
           if (ok && lt == 0 && piece > 0) ok = thread_wait(&hd->o_empty, (uint32_t)(piece - 1) & 1u, abort_flag);
           const uint32_t p_addr = smem_u32(p_s + (t & 1) * C::P_B);
-#pragma unroll 1
-          for (int i = 0; i < PB && ok; ++i) {
+          uint32_t at[PB];
+          const int vs0 = vs;
+#pragma unroll
+          for (int i = 0; i < PB; ++i) {
             if (!SAME)                    // K=V chunks have landed: the scores of this tile needed them
 #pragma unroll
               for (int j = 0; j < C::PER; ++j) ok = ok && thread_wait(&hd->full[bar0 + vs + j], vph, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t vd = sdesc_sw128(smem_u32(ring + vs * kTSlotBytes), C::CHUNK, 1024);
-            const uint64_t pd = sdesc_sw128(p_addr, 16, 1024);
+            at[i] = (smem_u32(ring) >> 4) + (uint32_t)vs * (kTSlotBytes >> 4);
+            vs += C::PER;
+            if (vs == slots) { vs = 0; vph ^= 1u; }
+          }
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t pd = sdesc_sw128(p_addr, 16, 1024), vdesc0 = sdesc_sw128(0, C::CHUNK, 1024);
+#pragma unroll
+          for (int i = 0; i < PB; ++i) {
+            const uint64_t vd = vdesc0 + at[i];
             const uint32_t d = tmem + C::COL_O + (uint32_t)((TG == 2 ? (t & 1) * PB : 0) + block_at<PB>(i)) * N;
 #pragma unroll
             for (int kk = 0; kk < KT / (E4M3 ? 32 : 16); ++kk) {
@@ -622,9 +648,11 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
               else umma_ss(d, vd + 128 * kk, pd + (kk >> 2) * (N * 8) + 2 * (kk & 3), id, acc);
             }
 #pragma unroll
-            for (int j = 0; j < C::PER; ++j) umma_commit(&hd->empty[bar0 + vs + j]);
-            vs += C::PER;
-            if (vs == slots) { vs = 0; vph ^= 1u; }
+            for (int j = 0; j < C::PER; ++j) {
+              int slot = vs0 + i * C::PER + j;
+              if (slot >= slots) slot -= slots;
+              umma_commit(&hd->empty[bar0 + slot]);
+            }
           }
           if (!ok) break;
           umma_commit(&hd->pv_done[t & 1]);
@@ -920,6 +948,24 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
       ok = warp_wait(&hd->hmeet[half], meets & 1u, abort_flag);
       ++meets;
     };
+    // e4m3: this thread's key's scales are read a tile of its group ahead, the table entry that leads
+    // to them two tiles ahead, past the ends of units too, so that no tile waits for either
+    float ks_next = 1.f, vs_next = 1.f;
+    int entry = -1;
+    auto read_entry = [&](const TilePiece& w, int lt) {
+      const int pos = (w.kt0 + lt) * KT + u;
+      entry = lt < w.ntiles && pos >= w.first && pos < w.end ? __ldg(a.c.table + (size_t)w.b * a.c.max_blocks + (pos >> a.c.page_shift)) : -1;
+    };
+    auto read_scales = [&](const TilePiece& w, int lt) {  // of tile lt, by its entry; and the next one's entry
+      const int pos = (w.kt0 + lt) * KT + u;
+      ks_next = vs_next = 1.f;
+      if ((unsigned)entry < (unsigned)a.c.num_pages) {
+        const size_t row = page_row(a.c, entry, w.kvh, pos & ((1 << a.c.page_shift) - 1));
+        ks_next = __ldg(a.c.k_scales + row);
+        if (!SAME) vs_next = __ldg(a.c.v_scales + row);
+      }
+      read_entry(w, lt + TG);
+    };
     int t0 = 0;                            // tiles of the units before
 #pragma unroll 1
     for (int piece = 0; ok && piece_at(piece, p); ++piece) {
@@ -936,29 +982,17 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
       // the references are the same in every lane and warp of the group; a copy in shared memory
       // serves what runs once in a while (the group meets before anyone reads it)
       if (quad == 0 && lane < H) hd->refs[piece & 1][half][0][lane] = hd->refs[piece & 1][half][1][lane] = -3.3e38f;
-      // e4m3: this thread's key's scales are read a tile ahead, the table entry that leads to
-      // them two tiles ahead, so that no tile waits for either
-      float ks_next = 1.f, vs_next = 1.f;
-      int entry = -1;
-      auto read_ahead = [&](int lt) {  // scales of tile lt, entry of the group's next
-        const int pos = (p.kt0 + lt) * KT + u, ps = a.c.page_shift;
-        ks_next = vs_next = 1.f;
-        if ((unsigned)entry < (unsigned)a.c.num_pages) {
-          const size_t row = page_row(a.c, entry, p.kvh, pos & ((1 << ps) - 1));
-          ks_next = __ldg(a.c.k_scales + row);
-          if (!SAME) vs_next = __ldg(a.c.v_scales + row);
-        }
-        const int np = pos + TG * KT;
-        entry = lt + TG < p.ntiles && np >= p.first && np < p.end ? __ldg(a.c.table + (size_t)p.b * a.c.max_blocks + (np >> ps)) : -1;
-      };
+      if (E4M3 && piece == 0) {
+        read_entry(p, lt0);
+        read_scales(p, lt0);
+      }
 #pragma unroll 1
-      for (int lt = E4M3 ? lt0 - 2 * TG : lt0; lt < p.ntiles && ok; lt += TG) {
+      for (int lt = lt0; lt < p.ntiles && ok; lt += TG) {
         float kscale = 1.f, vscale = 1.f;
         if constexpr (E4M3) {
           kscale = ks_next;
           vscale = SAME ? ks_next : vs_next;
-          read_ahead(lt + TG);
-          if (lt < 0) continue;
+          read_scales(p, lt + TG);
         }
         const int t = t0 + lt, bb = t & 1, k0 = (p.kt0 + lt) * KT;
         ok = warp_wait(&hd->s_full[bb], (uint32_t)(t >> 1) & 1u, abort_flag);
@@ -1114,6 +1148,14 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
         meet();
         if (!ok) break;
       }
+      // The next unit's first scales are read under this one's output.
+      const TilePiece& np = hd->piece[(piece + 1) & 7];
+      const int lt0_next = TG == 2 ? (half ^ (t0 + p.ntiles)) & 1 : 0;
+      if constexpr (E4M3) {
+        ok = warp_wait(&hd->piece_full[(piece + 1) & 7], (uint32_t)((piece + 1) >> 3) & 1u, abort_flag);
+        if (!ok) break;
+        read_entry(np, lt0_next);
+      }
       // The groups that share the rows meet: their sums and references are there to read.
       if (TG == 2) {
         if (lane == 0) mbar_arrive(&hd->o_meet);
@@ -1125,6 +1167,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
         ok = warp_wait(&hd->pv_done[(t0 - i) & 1], (uint32_t)((t0 - i) >> 1) & 1u, abort_flag);
       if (!ok) break;
       tc_fence_after();
+      if constexpr (E4M3) read_scales(np, lt0_next);
       // lane q forms row q's factors (of either group's output), log-sum-exp and place
       float fac[TG] = {};
       int place = -1;
