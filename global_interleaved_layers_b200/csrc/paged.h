@@ -1,6 +1,7 @@
 // paged.h -- the paged KV cache as the kernels see it, and the launch interfaces of the
 // paged-cache operators and of the draft verification.
 #pragma once
+#include <utility>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -71,6 +72,29 @@ __device__ __forceinline__ int seq_of_row(const int32_t* cu, int batch, int t) {
   return lo;
 }
 
+// The kernels of an attend call follow one another closely: each lets the next be launched as soon
+// as all its blocks run, and waits for the one before it to complete (and, through it, all before
+// that) ahead of its first access to global memory. That holds for the first one and whatever
+// kernel stands before it in the stream, too.
+__device__ __forceinline__ void follow() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_follower(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
 struct PagedAppendArgs {
   PagedCache c;
   const uint16_t* new_k;
@@ -79,7 +103,8 @@ struct PagedAppendArgs {
   const int32_t* lens;
   int batch, total_q;
   int r;                    // rotated pairs of the stored keys (0 for K=V)
-  double log2_base;
+  // theta_j / (2 pi) for j = 0, 8, 16, ..., and base^(-2 / d), from one pair's frequency to the next
+  double freq8[32], freq_step;
 };
 template <bool E4M3>
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
@@ -112,6 +137,8 @@ struct PagedAttendArgs {
   // row-group kernel: parts of cut units, two a team
   float* partial_o;         // [2 teams, 8, d]
   float* partial_lse;       // [2 teams, 8]
+  int4* joins;              // [teams]: the unit that a team's run begins and does not end (paged_merge_kernel)
+  const int* rest;          // beside chunk_of: sequences with rows that are not chunks
   int row_groups;           // most groups of 8 rows (query, head of the KV head's group) of a sequence
   const int* chunk_of;      // [batch], >= 0: the sequence is chunk_kernel's; null: there are none
   // set at the launch: units are cut into equal runs; teams; a run is a multiple of run_step;
@@ -141,7 +168,7 @@ cudaError_t launch_paged_merge(const PagedAttendArgs& a, cudaStream_t stream);
 // Long chunks (paged_chunk.cu): the device-side plan and the buffers it names, all in the
 // call's workspace.
 struct ChunkPlan {
-  int* header;              // [2]: entries of list, entries of merges
+  int* header;              // [3]: entries of list, entries of merges, sequences with rows that are not chunks
   int* chunk_of;            // [batch]: index among the chunk sequences, or -1
   int* tile0;               // [batch + 1]: first 128-position tile of the side copies
   int* unit0;               // [batch + 1]: first unit
@@ -166,7 +193,7 @@ struct ChunkMaps {
   CUtensorMap q, qs, k, k_rot, k_copy, v, v_copy;
 };
 cudaError_t launch_chunk(const ChunkMaps& maps, const PagedAttendArgs& a, const ChunkPlan& p, int units_bound,
-                         cudaStream_t stream);
+                         int slots, cudaStream_t stream);
 
 struct DraftArgs {
   const void* target;

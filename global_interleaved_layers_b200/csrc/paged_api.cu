@@ -52,7 +52,7 @@ constexpr int kChunkMinRows = 64;
 // How an attend call's work is cut, and what of the workspace each part takes (byte offsets).
 struct AttendPlan {
   PagedRowsShape shape;             // the sequences that are not chunks
-  size_t part_o, part_lse;
+  size_t part_o, part_lse, joins;
   bool chunk;                       // some sequence may have more rows than kChunkMinRows
   bool pair;
   int tokens, units_x, clusters, slots, units, seqs;
@@ -83,6 +83,7 @@ int attend_plan(const gemma_attn_params* p, bool e4m3, int batch, int total_q, i
   if (L->shape.cut) {
     L->part_o = take((size_t)L->shape.parts * L->shape.unit_rows * d * 4);
     L->part_lse = take((size_t)L->shape.parts * L->shape.unit_rows * 4);
+    L->joins = take((size_t)L->shape.parts / 2 * sizeof(int4));
   }
   if (L->chunk) {
     L->q_mask = rotated_chunk_mask(d, r);
@@ -102,7 +103,7 @@ int attend_plan(const gemma_attn_params* p, bool e4m3, int batch, int total_q, i
       L->tiles = std::min(most, ((long long)L->seqs * p->window + total_q) / 128 + 2ll * L->seqs + 1);
     L->copy_rows = e4m3 ? L->tiles * 128 : (long long)L->seqs * 256;
     if (L->tiles * 128 > 0x7fffffffll) return GEMMA_ATTN_ERR_UNSUPPORTED;
-    L->header = take(8);
+    L->header = take(12);
     L->chunk_of = take((size_t)batch * 4);
     L->tile0 = take(((size_t)batch + 1) * 4);
     L->unit0 = take(((size_t)batch + 1) * 4);
@@ -179,7 +180,7 @@ int launch_attend_chunks(const gemma_attn_params* params, const PagedAttendArgs&
   if (L.k_mask) ok &= box_map(&m.k_rot, p.k_rot, p.k_cols, p.rot_rows, hkv, keys, 1);
   if (!ok) return GEMMA_ATTN_ERR_LAUNCH;
   const long long units = (long long)(L.units + L.slots) * L.units_x;
-  return launch_chunk(m, a, p, (int)std::min<long long>(units, 1 << 20), stream) == cudaSuccess ? GEMMA_ATTN_OK : GEMMA_ATTN_ERR_LAUNCH;
+  return launch_chunk(m, a, p, (int)std::min<long long>(units, 1 << 20), L.slots, stream) == cudaSuccess ? GEMMA_ATTN_OK : GEMMA_ATTN_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -207,7 +208,11 @@ int gemma_attn_paged_append(const gemma_attn_params* params, const gemma_attn_pa
   a.batch = batch;
   a.total_q = total_q;
   a.r = params->kind == GEMMA_ATTN_LOCAL ? rotated_pairs(params->rope_p, params->head_dim) : 0;
-  a.log2_base = log2((double)params->rope_base);
+  if (a.r > 0) {
+    const double log2_step = -2.0 / params->head_dim * log2((double)params->rope_base);
+    for (int j = 0; j < a.r; j += 8) a.freq8[j / 8] = exp2(j * log2_step) * 0.15915494309189533577;  // 1 / (2 pi)
+    a.freq_step = exp2(log2_step);
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launched(e4m3 ? launch_paged_append<true>(a, s) : launch_paged_append<false>(a, s), 1);
 }
@@ -293,11 +298,13 @@ int gemma_attn_paged_attend(const gemma_attn_params* params, const gemma_attn_pa
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.partial_o = reinterpret_cast<float*>(ws + plan.part_o);
   a.partial_lse = reinterpret_cast<float*>(ws + plan.part_lse);
+  a.joins = reinterpret_cast<int4*>(ws + plan.joins);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int launches = plan.shape.cut ? 2 : 1;
   if (plan.chunk) {
     if (plan.seqs > 0) {
       a.chunk_of = reinterpret_cast<int*>(ws + plan.chunk_of);
+      a.rest = reinterpret_cast<int*>(ws + plan.header) + 2;
       rc = launch_attend_chunks(params, a, e4m3, plan, ws, s);
       if (rc != GEMMA_ATTN_OK) return rc;
       launches += 4;

@@ -127,11 +127,12 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PagedAttendArgs a, ChunkPlan p) {
   __shared__ int s_warp[32];
   __shared__ int s_hist[kPlanBuckets];
-  __shared__ int s_slots, s_merges;
+  __shared__ int s_slots, s_merges, s_rest;
   __shared__ unsigned long long s_work;
   const int tid = threadIdx.x;
+  follow();
   if (tid == 0) {
-    s_slots = s_merges = 0;
+    s_slots = s_merges = s_rest = 0;
     s_work = 0;
   }
   for (int i = tid; i < kPlanBuckets; i += kPlanThreads) s_hist[i] = 0;
@@ -155,6 +156,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PagedAttendArg
         is = 1;
         nt = hi - lo;
         nu = (n + p.tokens - 1) / p.tokens;
+      } else if (n > 0) {
+        s_rest = 1;
       }
     }
     int ti, tt, tu;
@@ -234,6 +237,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PagedAttendArg
   if (tid == 0) {
     p.header[0] = total;
     p.header[1] = s_merges;
+    p.header[2] = s_rest;
   }
 }
 
@@ -269,6 +273,7 @@ constexpr int kSideQHeads = 8;   // query heads of an item
 template <bool E4M3>
 __global__ void __launch_bounds__(kSideThreads) chunk_side_kernel(PagedAttendArgs a, ChunkPlan p) {
   __shared__ double s_freq[256];
+  follow();
   const int d = a.c.d, half = d / 2, groups = d / 16, hkv = a.c.hkv;
   for (int j = threadIdx.x; j < half; j += kSideThreads) s_freq[j] = j < a.r ? rope_inv_freq_turns(j, d, a.log2_base) : 0.0;
   __syncthreads();
@@ -433,6 +438,8 @@ __global__ void __launch_bounds__(kCThreads, 1)
 chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ PagedAttendArgs a,
              const __grid_constant__ ChunkPlan p) {
   using Cfg = ChunkCfg<D, PAIR>;
+  follow();
+  if (__ldcg(p.header) == 0) return;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_smem = smem;
@@ -969,40 +976,48 @@ chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ Pag
 // Join of cut units: a warp takes 128 columns of one row, the pieces in order.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) chunk_merge_kernel(PagedAttendArgs a, ChunkPlan p) {
+  follow();
+  if ((int)blockIdx.x >= __ldcg(p.header + 1)) return;
   const int lane = threadIdx.x & 31;
   const int D = a.c.d, chunks = (D + 127) / 128;
   const int rows = p.rows, tpc = kCM / a.group;          // rows of a unit (128 per CTA), tokens per 128
-  const long long per_unit = (long long)a.c.hkv * rows * chunks;
-  const long long total = (long long)p.header[1] * per_unit;
-  for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += (long long)gridDim.x * 8) {
-    const int4 e = __ldg(p.merges + i / per_unit);  // sequence, unit, first slot, pieces
-    const int in_unit = (int)(i % per_unit);
-    const int c0 = (in_unit % chunks) * 128 + lane * 4;
-    const int row = (in_unit / chunks) % rows, kvh = in_unit / (chunks * rows);
+  const int4 e = __ldcg(p.merges + blockIdx.x);          // sequence, unit, first slot, pieces
+  const int kvh = blockIdx.y;
+  const int tok0 = __ldg(a.cu_q + e.x), n = __ldg(a.cu_q + e.x + 1) - tok0;
+  const size_t head_step = (size_t)a.c.hkv * rows;       // from a piece's part to the next's
+#pragma unroll 1
+  for (int i = blockIdx.z * 8 + (threadIdx.x >> 5); i < rows * chunks; i += gridDim.z * 8) {
+    const int row = i / chunks, c0 = (i - row * chunks) * 128 + lane * 4;
     const int cta = row / kCM, r = row % kCM, rt = r / a.group;
-    const int tok0 = __ldg(a.cu_q + e.x), n = __ldg(a.cu_q + e.x + 1) - tok0;
     const int tok = e.y * p.tokens + cta * tpc + rt;
     if (rt >= tpc || tok >= n) continue;
-    float mm = -INFINITY;
-    bool nan = false;
-    for (int s = 0; s < e.w; ++s) {
-      const float l = p.part_lse[((size_t)(e.z + s) * a.c.hkv + kvh) * rows + row];
-      nan |= l != l;
-      mm = fmaxf(mm, l);
-    }
-    float den = 0.f;
+    const size_t pr0 = ((size_t)e.z * a.c.hkv + kvh) * rows + row;
+    // Up to 32 pieces at a time, a lane each, as paged_merge_kernel has it.
+    float mm = -INFINITY, den = 0.f, bad = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < e.w; ++s) {
-      const size_t pr = ((size_t)(e.z + s) * a.c.hkv + kvh) * rows + row;
-      const float l = p.part_lse[pr];
-      if (l == -INFINITY) continue;
-      const float w = nan ? l : __expf(l - mm);
-      den += w;
-      if (c0 < D) {
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + pr * D + c0);
-        acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
+    for (int s0 = 0; s0 < e.w; s0 += 32) {
+      const float l = s0 + lane < e.w ? __ldcg(p.part_lse + pr0 + (s0 + lane) * head_step) : -INFINITY;
+      if (__any_sync(0xffffffffu, l != l)) bad = NAN;
+      float m = fmaxf(mm, l);
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+      if (m == -INFINITY) continue;
+      const float old = __expf(mm - m), mine = l > -INFINITY ? __expf(l - m) : 0.f;
+      mm = m;
+      den *= old;
+      acc.x *= old; acc.y *= old; acc.z *= old; acc.w *= old;
+      const uint32_t live = __ballot_sync(0xffffffffu, l > -INFINITY);
+      const int count = min(32, e.w - s0);
+#pragma unroll 4
+      for (int k = 0; k < count; ++k) {
+        const float wt = __shfl_sync(0xffffffffu, mine, k);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (((live >> k) & 1u) && c0 < D) v = __ldcg(reinterpret_cast<const float4*>(p.part_o + (pr0 + (s0 + k) * head_step) * D + c0));
+        den += wt;
+        acc.x = fmaf(wt, v.x, acc.x); acc.y = fmaf(wt, v.y, acc.y); acc.z = fmaf(wt, v.z, acc.z); acc.w = fmaf(wt, v.w, acc.w);
       }
     }
+    den += bad;
     const size_t orow = ((size_t)tok0 + tok) * a.hq + kvh * a.group + (r - rt * a.group);
     if (c0 < D) {
       const float inv = den > 0.f || den != den ? 1.f / den : 0.f;
@@ -1026,26 +1041,25 @@ static cudaError_t launch_chunk_t(const ChunkMaps& maps, const PagedAttendArgs& 
   cfg.blockDim = dim3(kCThreads);
   cfg.dynamicSmemBytes = Cfg::kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  if (PAIR) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
   const int clusters = p.clusters < units_bound ? p.clusters : units_bound;
   cfg.gridDim = dim3((unsigned)(clusters * (PAIR ? 2 : 1)));
   return cudaLaunchKernelEx(&cfg, chunk_kernel<D, PAIR>, maps, a, p);
 }
 
 cudaError_t launch_chunk(const ChunkMaps& maps, const PagedAttendArgs& a, const ChunkPlan& p, int units_bound,
-                         cudaStream_t stream) {
-  chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, p);
-  if (p.e4m3) chunk_side_kernel<true><<<148 * 4, kSideThreads, 0, stream>>>(a, p);
-  else chunk_side_kernel<false><<<148 * 4, kSideThreads, 0, stream>>>(a, p);
-  cudaError_t e = cudaGetLastError();
+                         int slots, cudaStream_t stream) {
+  cudaError_t e = launch_follower(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a, p);
+  if (e != cudaSuccess) return e;
+  e = launch_follower(p.e4m3 ? chunk_side_kernel<true> : chunk_side_kernel<false>, dim3(kSms * 4), dim3(kSideThreads), 0, stream, a, p);
   if (e != cudaSuccess) return e;
   const bool pair = p.rows > kCM;
   switch (a.c.d) {
@@ -1056,8 +1070,9 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const PagedAttendArgs& a, const 
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
-  chunk_merge_kernel<<<148 * 2, 256, 0, stream>>>(a, p);
-  return cudaGetLastError();
+  // a unit that is cut has two pieces at least; a warp takes up to four rows' columns
+  const dim3 grid((unsigned)(slots / 2), (unsigned)a.c.hkv, (unsigned)((p.rows * ((a.c.d + 127) / 128) + 31) / 32));
+  return launch_follower(chunk_merge_kernel, grid, dim3(256), 0, stream, a, p);
 }
 
 }  // namespace gattn

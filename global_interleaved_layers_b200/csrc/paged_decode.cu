@@ -186,6 +186,12 @@ __device__ __forceinline__ int run_length(const PagedAttendArgs& a, int total) {
   return (int)((per + a.run_step - 1) / (uint32_t)a.run_step * a.run_step);
 }
 
+// What paged_merge_kernel is to join where `team`'s run ends inside a unit that begins in it:
+// {teams the unit runs over, first token, rows of the unit | KV head << 8, first row in the head}.
+__device__ __forceinline__ int4 join_of(int teams, int tok0, int rows, int kvh, int row0) {
+  return make_int4(teams, tok0, rows | kvh << 8, row0);
+}
+
 }  // namespace
 
 template <int D, bool E4M3, int NW, bool WARP_TEAMS>
@@ -196,6 +202,8 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
   constexpr int QST = D + 8;                       // 16-bit stride of a query row
   constexpr int RED = D + 4;
   constexpr int TW = WARP_TEAMS ? 1 : NW;          // warps of a team
+  follow();
+  if (a.rest != nullptr && __ldcg(a.rest) == 0) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tw = WARP_TEAMS ? 0 : warp;            // this warp's place in its team
   const int g = lane >> 2, t = lane & 3;
@@ -256,13 +264,15 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
 
   // ---- this team's run [x, x_end) of the line of blocks (cut) or units
   const int team = WARP_TEAMS ? (int)blockIdx.x * NW + warp : (int)blockIdx.x;
-  int b, before, x, x_end;
+  int b, before, x, x_end, run_len;
   {
     const int total = line_find(a, lane, a.cut ? -1 : team, &b, &before);
     const int run = run_length(a, total);
     x = min((long long)team * run, (long long)total);
     x_end = a.cut ? (int)min((long long)total, (long long)x + run) : total;   // uncut: units team, team + teams, ...
     if (x < x_end && a.cut) line_find(a, lane, x, &b, &before);
+    if (a.cut && tw == 0 && lane == 0) a.joins[team] = make_int4(0, 0, 0, 0);
+    run_len = run;
   }
 
   int st = 0, sv = 0;               // stage of the next block's keys and values
@@ -285,6 +295,8 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
     const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0, len = __ldg(a.lens + b);
     const int rows = min(kPR, n * a.group - row0);
     const int first = keys_first(a, len, 0), end = len + n, blk0 = first / kPB;
+    if (a.cut && b_lo == 0 && b_hi < blocks && tw == 0 && lane == 0)
+      a.joins[team] = join_of((x + blocks - 1) / run_len - team + 1, tok0, rows, kvh, row0);
     x += a.cut ? b_hi - b_lo : a.teams;
 
     // blocks of this warp: b_lo + tw, + TW, ...
@@ -813,37 +825,29 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
 
 // ---------------------------------------------------------------------------
 // Join of cut units: out = sum_s exp(lse_s - M) o_s / sum_s exp(lse_s - M) over the teams whose runs
-// the unit crosses, in order. A block takes a border between two runs; the unit that it cuts is
-// joined there if no earlier border cuts it. A warp takes 128 columns of one row, four per lane.
-// (Walking all rows of the call instead, to find the few of cut units, took 167 us of a call of
-// three prompt chunks, which has none.)
+// the unit crosses, in order. A block (or a few) takes the unit that one team's run begins and does
+// not end, which the team has left a note of: finding such units again from the lengths cost 20
+// to 35 us, mostly instruction fetch. A warp takes 128 columns of one row, four per lane.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) paged_merge_kernel(PagedAttendArgs a) {
+  follow();
+  if (a.rest != nullptr && __ldcg(a.rest) == 0) return;
   const int lane = threadIdx.x & 31;
+  const int4 j = __ldcg(a.joins + blockIdx.x);
+  if (j.x == 0) return;
   const int D = a.c.d, ur = a.unit_rows, chunks = (D + 127) / 128;
-  int b, before, blocks, units;
-  const int total = line_find(a, lane, -1, &b, &before);
-  const int run = run_length(a, total);
-  const long long x = (long long)(blockIdx.x + 1) * run;  // the border
-  if (x >= total) return;
-  line_find(a, lane, (int)x, &b, &before);
-  seq_units(a, b, &blocks, &units);
-  const int u = ((int)x - before) / blocks, x0 = before + u * blocks, w0 = x0 / run;
-  if (x0 == x || w0 != (int)blockIdx.x) return;  // nothing is cut, or an earlier border joins it
-  const int w1 = (x0 + blocks - 1) / run;
-  const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0;
-  const int row0 = u / a.c.hkv * ur, rows = min(ur, n * a.group - row0);
+  const int w0 = blockIdx.x, w1 = w0 + j.x - 1, rows = j.z & 255, kvh = j.z >> 8, row0 = j.w;
 #pragma unroll 1
   for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < rows * chunks; i += gridDim.y * 8) {
     const int ri = i / chunks, c0 = i % chunks * 128 + lane * 4, in_head = row0 + ri;  // row within the KV head
     const int tk = in_head / a.group;
-    const size_t row = ((size_t)tok0 + tk) * a.hq + u % a.c.hkv * a.group + (in_head - tk * a.group);
+    const size_t row = ((size_t)j.y + tk) * a.hq + kvh * a.group + (in_head - tk * a.group);
     auto at = [&](int w) { return ((size_t)2 * w + (w == w0 ? 1 : 0)) * ur + ri; };
     // Up to 32 parts at a time, a lane each; the reference is the largest of those seen so far.
     float mm = -INFINITY, den = 0.f, bad = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int wb = w0; wb <= w1; wb += 32) {
-      const float l = wb + lane <= w1 ? a.partial_lse[at(wb + lane)] : -INFINITY;
+      const float l = wb + lane <= w1 ? __ldcg(a.partial_lse + at(wb + lane)) : -INFINITY;
       if (__any_sync(0xffffffffu, l != l)) bad = NAN;
       float m = fmaxf(mm, l);
 #pragma unroll
@@ -859,7 +863,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(PagedAttendArgs a) {
       for (int k = 0; k < count; ++k) {
         const float wt = __shfl_sync(0xffffffffu, mine, k);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (((live >> k) & 1u) && c0 < D) v = __ldg(reinterpret_cast<const float4*>(a.partial_o + at(wb + k) * D + c0));
+        if (((live >> k) & 1u) && c0 < D) v = __ldcg(reinterpret_cast<const float4*>(a.partial_o + at(wb + k) * D + c0));
         den += wt;
         acc.x = fmaf(wt, v.x, acc.x); acc.y = fmaf(wt, v.y, acc.y); acc.z = fmaf(wt, v.z, acc.z); acc.w = fmaf(wt, v.w, acc.w);
       }
@@ -878,9 +882,8 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(PagedAttendArgs a) {
 
 cudaError_t launch_paged_merge(const PagedAttendArgs& a, cudaStream_t stream) {
   if (a.teams < 2) return cudaSuccess;
-  const dim3 grid(a.teams - 1, (a.unit_rows * ((a.c.d + 127) / 128) + 31) / 32);  // up to four rows' columns a warp
-  paged_merge_kernel<<<grid, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  const dim3 grid(a.teams - 1, (a.unit_rows * ((a.c.d + 127) / 128) + 7) / 8);
+  return launch_follower(paged_merge_kernel, grid, dim3(256), 0, stream, a);
 }
 
 // Teams for a call: `units` units of at most `max_blocks` blocks, `group_rows` rows in a group.
@@ -934,15 +937,13 @@ static cudaError_t launch_paged_rows_t(PagedAttendArgs a, const PagedRowsShape& 
     if (f.warp_teams) {
       e = allow_smem(paged_rows_kernel<D, E4M3, NW, true>, kPMaxSmem, ready[1]);
       if (e != cudaSuccess) return e;
-      paged_rows_kernel<D, E4M3, NW, true><<<grid, NW * 32, smem, stream>>>(a, f);
-      e = cudaGetLastError();
+      e = launch_follower(paged_rows_kernel<D, E4M3, NW, true>, dim3(grid), dim3(NW * 32), smem, stream, a, f);
     }
   }
   if (!f.warp_teams) {
     e = allow_smem(paged_rows_kernel<D, E4M3, NW, false>, kPMaxSmem, ready[0]);
     if (e != cudaSuccess) return e;
-    paged_rows_kernel<D, E4M3, NW, false><<<grid, NW * 32, smem, stream>>>(a, f);
-    e = cudaGetLastError();
+    e = launch_follower(paged_rows_kernel<D, E4M3, NW, false>, dim3(grid), dim3(NW * 32), smem, stream, a, f);
   }
   if (e != cudaSuccess || !f.cut) return e;
   return launch_paged_merge(a, stream);

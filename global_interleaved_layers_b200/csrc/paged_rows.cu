@@ -10,10 +10,12 @@
 // 2^-4 of the value), and the kernels that read the pages may fold s into a product.
 // Gather is the way back: code * s.
 //
-// Both are bound by HBM for long chunks and by launch latency for a decode step's few rows. A
-// group of d / 16 lanes owns one (row, KV head, tensor), 16 elements a lane in two runs of 8 that
-// hold both members of 8 pairs: 32 bytes in and 16 (or 32) out per lane, and the row's
-// maximum is a shuffle within the group. Whole warps are filled for every head dim.
+// Both are bound by HBM for long chunks and by latency for a decode step's few rows: launch,
+// instruction fetch (the kernels are kept small for it) and the chain from a row to its sequence,
+// length, page and data. A group of d / 16 lanes owns a row's 4 heads of one tensor, 16 elements
+// a lane and head in two runs of 8 that hold both members of 8 pairs; the heads share the row's
+// place and angles and have their loads in flight together, and a maximum is a shuffle within
+// the group. Whole warps are filled for every head dim.
 #include "paged.h"
 
 namespace gattn {
@@ -21,6 +23,7 @@ namespace gattn {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kRowHeads = 4;      // heads of a group of lanes
 
 __device__ __forceinline__ void bf8_to_f32(const uint4& w, float* f) {
   const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
@@ -77,167 +80,208 @@ __device__ __forceinline__ float row_scale(float amax, float* inv) {
   return __uint_as_float((uint32_t)(127 + k) << 23);
 }
 
+// Sequence of row t, as seq_of_row, by a group of G lanes (of whole warps that call together): G
+// probes a step instead of one, since each step costs a memory latency.
+__device__ __forceinline__ int group_seq_of_row(const int32_t* cu, int batch, int t, int G) {
+  const int lane = threadIdx.x & 31, in_group = lane & (G - 1), first = lane - in_group;
+  const uint32_t mine = (G == 32 ? 0xffffffffu : (1u << G) - 1u) << first;
+  int lo = 0, hi = batch;  // cu[lo] <= t < cu[hi]
+  while (__any_sync(0xffffffffu, hi - lo > 1)) {
+    const int step = (hi - lo + G) / (G + 1), probe = lo + (in_group + 1) * step;
+    const bool le = probe < hi && __ldg(cu + probe) <= t;
+    lo += __popc(__ballot_sync(0xffffffffu, le) & mine) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+__device__ __noinline__ float2 row_turn(double pos, double inv_freq_turns) {
+  float2 r;
+  rope_cos_sin(pos, inv_freq_turns, &r.x, &r.y);
+  return r;
+}
+
+// Place of a row: sequence and position; false when it has none (the status then says why).
+__device__ __forceinline__ bool row_place(const PagedCache& c, const int32_t* cu, const int32_t* base, int batch, int t, bool in,
+                                          int G, bool first_lane, int* b, int* pos) {
+  *b = group_seq_of_row(cu, batch, t, G);
+  const int tok0 = __ldg(cu + *b);
+  const long long p = (long long)__ldg(base + *b) + (t - tok0);
+  *pos = (int)p;
+  if (!in || t < tok0) return false;  // past the last row, or before the first sequence
+  if (p < 0 || p >= ((long long)c.max_blocks << c.page_shift)) {
+    if (first_lane) atomicOr(&g_status, kStatusSeqlen);
+    return false;
+  }
+  return true;
+}
+
 }  // namespace
 
 template <bool E4M3>
 __global__ void __launch_bounds__(kRowThreads) paged_append_kernel(PagedAppendArgs a) {
   const int d = a.c.d, group = d / 16;              // 4, 8, 16 or 32 lanes: never across a warp
-  const int tensors = a.c.v != nullptr ? 2 : 1;
-  const long long unit = ((long long)blockIdx.x * kRowThreads + threadIdx.x) / group;
+  const bool is_v = blockIdx.y != 0;
+  const int hkv = a.c.hkv, hb = (hkv + kRowHeads - 1) / kRowHeads;
+  const uint32_t unit = (blockIdx.x * kRowThreads + threadIdx.x) / group;  // (rows that fit in memory number under 2^31)
   const int c8 = ((int)threadIdx.x & (group - 1)) * 8;
-  const int hkv = a.c.hkv;
-  const long long units = (long long)min(a.total_q, __ldg(a.cu_q + a.batch)) * hkv * tensors;
-  const bool in = unit < units;  // lanes past the end stay for the group's shuffles
-  const long long rest = in ? unit / tensors : 0;
-  const bool is_v = in && unit % tensors != 0;
-  const int t = (int)(rest / hkv), head = (int)(rest % hkv);
-  bool ok = in;
-  int pos = 0, b = 0;
-  if (in) {
-    b = seq_of_row(a.cu_q, a.batch, t);
-    const long long p = (long long)__ldg(a.lens + b) + (t - __ldg(a.cu_q + b));
-    if (t < __ldg(a.cu_q + b)) {  // before the first sequence
-      ok = false;
-    } else if (p < 0 || p >= ((long long)a.c.max_blocks << a.c.page_shift)) {
-      if (c8 == 0) atomicOr(&g_status, kStatusSeqlen);
-      ok = false;
-    } else {
-      pos = (int)p;
-    }
+  const int t = unit / hb, h0 = (int)(unit - (uint32_t)t * hb) * kRowHeads;
+  const bool in = t < min(a.total_q, __ldg(a.cu_q + a.batch));  // lanes past the end stay for the group's shuffles
+  int pos, b;
+  bool ok = row_place(a.c, a.cu_q, a.lens, a.batch, t, in, group, c8 == 0, &b, &pos);
+  uint4 w0[kRowHeads], w1[kRowHeads];
+  const uint16_t* src = (is_v ? a.new_v : a.new_k) + ((size_t)t * hkv + h0) * d + c8;
+#pragma unroll
+  for (int k = 0; k < kRowHeads; ++k) {
+    const bool get = ok && h0 + k < hkv;
+    w0[k] = get ? __ldg(reinterpret_cast<const uint4*>(src + k * d)) : make_uint4(0u, 0u, 0u, 0u);
+    w1[k] = get ? __ldg(reinterpret_cast<const uint4*>(src + k * d + d / 2)) : make_uint4(0u, 0u, 0u, 0u);
   }
-  size_t dst = 0;
-  float x0[8] = {}, x1[8] = {};
-  if (ok) {
-    const int page = page_of(a.c, b, pos >> a.c.page_shift);
-    if (page < 0) {
-      ok = false;
-    } else {
-      dst = page_row(a.c, page, head, pos & ((1 << a.c.page_shift) - 1));
-      const uint16_t* src = (is_v ? a.new_v : a.new_k) + ((size_t)t * hkv + head) * d;
-      bf8_to_f32(__ldg(reinterpret_cast<const uint4*>(src + c8)), x0);
-      bf8_to_f32(__ldg(reinterpret_cast<const uint4*>(src + d / 2 + c8)), x1);
-    }
-  }
-  if (!is_v && ok && c8 < a.r) {
+  int page = ok ? __ldg(a.c.table + (size_t)b * a.c.max_blocks + (pos >> a.c.page_shift)) : -1;
+  float2 turn[8];
+  const bool rot = !is_v && ok && c8 < a.r;
+  if (rot) {
+    double f = a.freq8[c8 / 8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int j = c8 + e;
-      if (j < a.r) {
-        float cs, sn;
-        rope_cos_sin((double)pos, rope_inv_freq_turns(j, d, a.log2_base), &cs, &sn);
-        const float y0 = x0[e] * cs - x1[e] * sn;
-        x1[e] = x0[e] * sn + x1[e] * cs;
+      turn[e] = c8 + e < a.r ? row_turn((double)pos, f) : make_float2(1.f, 0.f);
+      f *= a.freq_step;
+    }
+  }
+  if (ok && (unsigned)page >= (unsigned)a.c.num_pages) {
+    atomicOr(&g_status, kStatusPage);
+    ok = false;
+  }
+  const size_t dst0 = ok ? page_row(a.c, page, h0, pos & ((1 << a.c.page_shift) - 1)) : 0;
+#pragma unroll
+  for (int k = 0; k < kRowHeads; ++k) {
+    const bool put = ok && h0 + k < hkv;
+    const size_t dst = dst0 + ((size_t)k << a.c.page_shift);
+    float x0[8], x1[8];
+    bf8_to_f32(w0[k], x0);
+    bf8_to_f32(w1[k], x1);
+    if (rot) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y0 = x0[e] * turn[e].x - x1[e] * turn[e].y;
+        x1[e] = x0[e] * turn[e].y + x1[e] * turn[e].x;
         x0[e] = y0;
       }
     }
-  }
-  if constexpr (E4M3) {
-    // as bit patterns, |x| orders like an unsigned integer and NaN above infinity
-    uint32_t top = 0;
+    if constexpr (E4M3) {
+      // as bit patterns, |x| orders like an unsigned integer and NaN above infinity
+      uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      top = max(top, max(__float_as_uint(x0[e]) & 0x7FFFFFFFu, __float_as_uint(x1[e]) & 0x7FFFFFFFu));
-    for (int m = group / 2; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-    float inv;
-    const float scale = row_scale(__uint_as_float(top), &inv);
-    if (!ok) return;
-    const bool bad = top >= 0x7F800000u;  // codes of a NaN-scaled row: zero
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x0[e] = bad ? 0.f : x0[e] * inv;
-      x1[e] = bad ? 0.f : x1[e] * inv;
-    }
-    if (scale == 0x1p120f) {  // 248 .. 255 would round to 256, and 256 * 2^120 is past fp32's range
+      for (int e = 0; e < 8; ++e)
+        top = max(top, max(__float_as_uint(x0[e]) & 0x7FFFFFFFu, __float_as_uint(x1[e]) & 0x7FFFFFFFu));
+#pragma unroll 1
+      for (int m = group / 2; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+      float inv;
+      const float scale = row_scale(__uint_as_float(top), &inv);
+      const bool bad = top >= 0x7F800000u;  // codes of a NaN-scaled row: zero
+      // at scale 2^120, 248 .. 255 would round to 256, and 256 * 2^120 is past fp32's range
+      const float most = scale == 0x1p120f ? 240.f : 448.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x0[e] = fminf(fmaxf(x0[e], -240.f), 240.f);
-        x1[e] = fminf(fmaxf(x1[e], -240.f), 240.f);
+        x0[e] = bad ? 0.f : fminf(fmaxf(x0[e] * inv, -most), most);
+        x1[e] = bad ? 0.f : fminf(fmaxf(x1[e] * inv, -most), most);
       }
+      if (!put) continue;
+      uint8_t* out = (is_v ? a.c.v : a.c.k) + dst * d;
+      *reinterpret_cast<uint2*>(out + c8) = f32_to_e4m3x8(x0);
+      *reinterpret_cast<uint2*>(out + d / 2 + c8) = f32_to_e4m3x8(x1);
+      if (c8 == 0) (is_v ? a.c.v_scales : a.c.k_scales)[dst] = scale;
+    } else {
+      if (!put) continue;
+      uint16_t* out = reinterpret_cast<uint16_t*>(is_v ? a.c.v : a.c.k) + dst * d;
+      *reinterpret_cast<uint4*>(out + c8) = f32_to_bf8(x0);
+      *reinterpret_cast<uint4*>(out + d / 2 + c8) = f32_to_bf8(x1);
     }
-    uint8_t* out = (is_v ? a.c.v : a.c.k) + dst * d;
-    *reinterpret_cast<uint2*>(out + c8) = f32_to_e4m3x8(x0);
-    *reinterpret_cast<uint2*>(out + d / 2 + c8) = f32_to_e4m3x8(x1);
-    if (c8 == 0) (is_v ? a.c.v_scales : a.c.k_scales)[dst] = scale;
-  } else {
-    if (!ok) return;
-    uint16_t* out = reinterpret_cast<uint16_t*>(is_v ? a.c.v : a.c.k) + dst * d;
-    *reinterpret_cast<uint4*>(out + c8) = f32_to_bf8(x0);
-    *reinterpret_cast<uint4*>(out + d / 2 + c8) = f32_to_bf8(x1);
   }
+}
+
+// Grid of a rows kernel, a tensor per y; 0 blocks: nothing to do.
+static cudaError_t rows_grid(const PagedCache& c, int rows, dim3* grid) {
+  const long long lanes = (long long)rows * ((c.hkv + kRowHeads - 1) / kRowHeads) * (c.d / 16);
+  const long long blocks = (lanes + kRowThreads - 1) / kRowThreads;
+  if (lanes / (c.d / 16) > 0x7fffffffll || blocks > 0x00ffffffll) return cudaErrorInvalidValue;
+  *grid = dim3((unsigned)blocks, c.v != nullptr ? 2 : 1);
+  return cudaSuccess;
 }
 
 template <bool E4M3>
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
-  const long long lanes = (long long)a.total_q * a.c.hkv * (a.c.v ? 2 : 1) * (a.c.d / 16);
-  if (lanes == 0) return cudaSuccess;
-  const long long blocks = (lanes + kRowThreads - 1) / kRowThreads;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  paged_append_kernel<E4M3><<<(unsigned)blocks, kRowThreads, 0, stream>>>(a);
+  dim3 grid;
+  const cudaError_t e = rows_grid(a.c, a.total_q, &grid);
+  if (e != cudaSuccess || grid.x == 0) return e;
+  paged_append_kernel<E4M3><<<grid, kRowThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 template <bool E4M3, bool F32>
 __global__ void __launch_bounds__(kRowThreads) paged_gather_kernel(PagedGatherArgs a) {
   const int d = a.c.d, group = d / 16;
-  const int tensors = a.c.v != nullptr ? 2 : 1;
-  const long long unit = ((long long)blockIdx.x * kRowThreads + threadIdx.x) / group;
+  const bool is_v = blockIdx.y != 0;
+  const int hkv = a.c.hkv, hb = (hkv + kRowHeads - 1) / kRowHeads;
+  const uint32_t unit = (blockIdx.x * kRowThreads + threadIdx.x) / group;
   const int c16 = ((int)threadIdx.x & (group - 1)) * 16;
-  const int hkv = a.c.hkv;
-  const long long units = (long long)min(a.total_out, __ldg(a.cu_out + a.batch)) * hkv * tensors;
-  if (unit >= units) return;
-  const long long rest = unit / tensors;
-  const bool is_v = unit % tensors != 0;
-  const int t = (int)(rest / hkv), head = (int)(rest % hkv);
-  const int b = seq_of_row(a.cu_out, a.batch, t);
-  if (t < __ldg(a.cu_out + b)) return;  // before the first sequence
-  const long long p = (long long)__ldg(a.starts + b) + (t - __ldg(a.cu_out + b));
-  int page = -1;
-  if (p < 0 || p >= ((long long)a.c.max_blocks << a.c.page_shift)) {
-    if (c16 == 0) atomicOr(&g_status, kStatusSeqlen);
-  } else {
-    page = page_of(a.c, b, (int)(p >> a.c.page_shift));
-  }
-  float f[16] = {};
-  uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
-  if (page >= 0) {
-    const size_t src = page_row(a.c, page, head, (int)p & ((1 << a.c.page_shift) - 1));
+  const int t = unit / hb, h0 = (int)(unit - (uint32_t)t * hb) * kRowHeads;
+  const bool in = t < min(a.total_out, __ldg(a.cu_out + a.batch));
+  int pos, b;
+  const bool ok = row_place(a.c, a.cu_out, a.starts, a.batch, t, in, group, c16 == 0, &b, &pos);
+  if (!in || t < __ldg(a.cu_out + b)) return;
+  const int page = ok ? page_of(a.c, b, pos >> a.c.page_shift) : -1;  // rows without a place: zeros
+  const size_t src0 = page >= 0 ? page_row(a.c, page, h0, pos & ((1 << a.c.page_shift) - 1)) : 0;
+  uint4 w0[kRowHeads], w1[kRowHeads];
+  float s[kRowHeads];
+#pragma unroll
+  for (int k = 0; k < kRowHeads; ++k) {
+    w0[k] = w1[k] = make_uint4(0u, 0u, 0u, 0u);
+    s[k] = 0.f;
+    if (page < 0 || h0 + k >= hkv) continue;
+    const size_t src = src0 + ((size_t)k << a.c.page_shift);
     const uint8_t* base = (is_v ? a.c.v : a.c.k) + src * d * (E4M3 ? 1 : 2);
     if constexpr (E4M3) {
-      w0 = __ldg(reinterpret_cast<const uint4*>(base + c16));
-      const float s = __ldg((is_v ? a.c.v_scales : a.c.k_scales) + src);
-      const uint32_t ws[4] = {w0.x, w0.y, w0.z, w0.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) e4m3x4_to_f32(ws[k], f + 4 * k);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) f[e] *= s;
+      w0[k] = __ldg(reinterpret_cast<const uint4*>(base + c16));
+      s[k] = __ldg((is_v ? a.c.v_scales : a.c.k_scales) + src);
     } else {
-      w0 = __ldg(reinterpret_cast<const uint4*>(base + 2 * c16));
-      w1 = __ldg(reinterpret_cast<const uint4*>(base + 2 * c16 + 16));
-      if constexpr (F32) {
-        bf8_to_f32(w0, f);
-        bf8_to_f32(w1, f + 8);
-      }
+      w0[k] = __ldg(reinterpret_cast<const uint4*>(base + 2 * c16));
+      w1[k] = __ldg(reinterpret_cast<const uint4*>(base + 2 * c16 + 16));
     }
   }
-  const size_t dst = ((size_t)t * hkv + head) * d + c16;
-  if constexpr (F32) {
-    float* out = static_cast<float*>(is_v ? a.out_v : a.out_k) + dst;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) *reinterpret_cast<float4*>(out + 4 * k) = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
-  } else {
-    uint16_t* out = static_cast<uint16_t*>(is_v ? a.out_v : a.out_k) + dst;
-    *reinterpret_cast<uint4*>(out) = E4M3 ? f32_to_bf8(f) : w0;
-    *reinterpret_cast<uint4*>(out + 8) = E4M3 ? f32_to_bf8(f + 8) : w1;
+  for (int k = 0; k < kRowHeads; ++k) {
+    if (h0 + k >= hkv) break;
+    float f[16];
+    if constexpr (E4M3) {
+      const uint32_t ws[4] = {w0[k].x, w0[k].y, w0[k].z, w0[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e4m3x4_to_f32(ws[i], f + 4 * i);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) f[e] *= s[k];
+    } else if constexpr (F32) {
+      bf8_to_f32(w0[k], f);
+      bf8_to_f32(w1[k], f + 8);
+    }
+    const size_t dst = ((size_t)t * hkv + h0 + k) * d + c16;
+    if constexpr (F32) {
+      float* out = static_cast<float*>(is_v ? a.out_v : a.out_k) + dst;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(out + 4 * i) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+    } else {
+      uint16_t* out = static_cast<uint16_t*>(is_v ? a.out_v : a.out_k) + dst;
+      *reinterpret_cast<uint4*>(out) = E4M3 ? f32_to_bf8(f) : w0[k];
+      *reinterpret_cast<uint4*>(out + 8) = E4M3 ? f32_to_bf8(f + 8) : w1[k];
+    }
   }
 }
 
 template <bool E4M3, bool F32>
 cudaError_t launch_paged_gather(const PagedGatherArgs& a, cudaStream_t stream) {
-  const long long lanes = (long long)a.total_out * a.c.hkv * (a.c.v ? 2 : 1) * (a.c.d / 16);
-  if (lanes == 0) return cudaSuccess;
-  const long long blocks = (lanes + kRowThreads - 1) / kRowThreads;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  paged_gather_kernel<E4M3, F32><<<(unsigned)blocks, kRowThreads, 0, stream>>>(a);
+  dim3 grid;
+  const cudaError_t e = rows_grid(a.c, a.total_out, &grid);
+  if (e != cudaSuccess || grid.x == 0) return e;
+  paged_gather_kernel<E4M3, F32><<<grid, kRowThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -261,14 +261,15 @@ __device__ __noinline__ float2 turn_of(double pos, double inv_freq_turns) {
 // The CTA's pieces in turn, by one warp: units team, team + teams, ..., or a run of the line of
 // all units' tiles.
 struct TileWalk {
-  int x, x_end, before, b;
+  int x, x_end, before, b, run;
   __device__ __forceinline__ void start(const PagedAttendArgs& a, int lane) {
     const int team = blockIdx.x;
     const int total = line_find(a, lane, a.cut ? -1 : team, &b, &before);
-    const int run = run_length(a, total);
+    run = run_length(a, total);
     x = (int)min((long long)team * run, (long long)total);
     x_end = a.cut ? (int)min((long long)total, (long long)x + run) : total;
     if (a.cut && x < x_end) line_find(a, lane, x, &b, &before);
+    if (a.cut && lane == 0) a.joins[team] = make_int4(0, 0, 0, 0);
   }
   __device__ __forceinline__ void next(const PagedAttendArgs& a, int lane, TilePiece& p) {
     p.ntiles = 0;
@@ -295,6 +296,8 @@ struct TileWalk {
     p.kt0 = (p.first >> a.unit_shift) + lo;
     p.ntiles = hi - lo;
     p.pad = 0;
+    if (p.slot >= 0 && lo == 0 && lane == 0)
+      a.joins[blockIdx.x] = join_of((x + blocks - 1) / run - (int)blockIdx.x + 1, p.tok0, p.rows, p.kvh, p.row0);
     x += a.cut ? p.ntiles : a.teams;
   }
 };
@@ -343,6 +346,8 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
   constexpr int G = C::G, NS = C::NS, TG = C::TG;
   // slot of a tile that holds the second half's rotated dims (the first holds the first half's)
   constexpr int ROT2 = G == 2 ? 1 : E4M3 ? (PB > 1 ? 1 : 0) : (PB > 1 ? 2 : 1);
+  follow();
+  if (a.rest != nullptr && __ldcg(a.rest) == 0) return;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   using Header = TileHeader<SG, H>;
@@ -1298,8 +1303,7 @@ static cudaError_t launch_tile_t(PagedAttendArgs a, bool cut, long long units, c
   a.run_step = 1;
   a.unit_rows = C::NR;
   a.unit_shift = C::KT == 128 ? 7 : 6;
-  paged_tile_kernel<D, E4M3, SAME, SG, H><<<grid, kTThreads, 232448, stream>>>(k, v, a, tile_turns(D, a.log2_base));
-  e = cudaGetLastError();
+  e = launch_follower(paged_tile_kernel<D, E4M3, SAME, SG, H>, dim3(grid), dim3(kTThreads), 232448, stream, k, v, a, tile_turns(D, a.log2_base));
   if (e != cudaSuccess || !cut) return e;
   return launch_paged_merge(a, stream);
 }
