@@ -477,7 +477,7 @@ chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ Pag
   };
 
   if (threadIdx.x == 0) {
-    const uint32_t loads = PAIR ? 2u : 1u;
+    const uint32_t loads = PAIR && leader ? 2u : 1u;  // the even CTA's barriers count the odd CTA's word too
     mbar_init(&bars->q_full, loads);
     mbar_init(&bars->q_empty, 1);
     for (int b = 0; b < 2; ++b) {
@@ -523,13 +523,8 @@ chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ Pag
     // One thread, by elect.sync: a copy issued by divergent lanes costs some 200 cycles, and with
     // pages of 16 a tile takes 32 boxes.
     if (elect_one()) {
-      auto expect = [&](uint64_t* bar, uint32_t bytes) {
-        if (!PAIR || leader) mbar_arrive_expect_tx(bar, bytes);
-        else mbar_arrive_expect_tx_cluster(smem_u32(bar) & kPeerBitMask, bytes);
-      };
       auto load = [&](void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
-        if constexpr (PAIR) tma_load_3d_pair(dst, map, bar, c0, c1, c2);
-        else tma_load_3d(dst, map, bar, c0, c1, c2);
+        tma_load_3d(dst, map, bar, c0, c1, c2);
       };
       auto col_of = [](uint32_t mask, int c) { return __popc(mask & ((1u << c) - 1u)) * 64; };
       const int ps = 1 << a.c.page_shift;
@@ -549,7 +544,7 @@ chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ Pag
           ok = mbar_wait(&bars->q_empty, (uint32_t)(unit_iter - 1) & 1u, abort_flag);
           if (!ok) break;
         }
-        expect(&bars->q_full, Cfg::kQChunks * 128u * (uint32_t)(tpc * a.group));
+        mbar_arrive_expect_tx(&bars->q_full, Cfg::kQChunks * 128u * (uint32_t)(tpc * a.group));
 #pragma unroll 1
         for (int c = 0; c < Cfg::kQChunks; ++c) {
           const bool rot = (p.q_mask >> c) & 1u;
@@ -600,7 +595,7 @@ chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ Pag
               ok = mbar_wait(&bars->ring_empty[st], ph ^ 1u, abort_flag);
               if (!ok) break;
               uint64_t* bar = &bars->ring_full[st];
-              expect(bar, Cfg::kStageBytes);
+              mbar_arrive_expect_tx(bar, Cfg::kStageBytes);
               uint8_t* dst = ring + st * Cfg::kStageBytes;
               const int c0 = Cfg::kKPerStage * s;
               const uint32_t side = cr >= 0 ? ~0u : p.k_mask >> c0;  // chunks that are not read from the pages
@@ -635,7 +630,7 @@ chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ Pag
               ok = mbar_wait(&bars->ring_empty[st], ph ^ 1u, abort_flag);
               if (!ok) break;
               uint64_t* bar = &bars->ring_full[st];
-              expect(bar, Cfg::kStageBytes);
+              mbar_arrive_expect_tx(bar, Cfg::kStageBytes);
               uint8_t* dst = ring + st * Cfg::kStageBytes;
               const int col = w.part * Cfg::kDv + (PAIR ? 2 * s + (int)rank : s) * Cfg::kVPerStage * 64;
               if (cr >= 0) {
@@ -658,10 +653,9 @@ chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ Pag
         }
         ++unit_iter;
       }
-      // Copies counted on this CTA's barriers land before it can leave: the last fill of each
-      // slot (its phase has parity ph ^ 1 in the order walked here) and the last Q. The odd CTA's
-      // copies complete on the even CTA's barriers, which waits for them before the pair leaves.
-      if (!PAIR || leader) {
+      // This CTA's copies land before it can leave: the last fill of each slot (its phase has parity
+      // ph ^ 1 in the order walked here) and the last Q.
+      {
         for (int s = 0; s < Cfg::kStages; ++s) {
           const unsigned long long w0 = globaltimer_ns();
           while (!mbar_try_wait(&bars->ring_full[st], ph ^ 1u) && globaltimer_ns() - w0 < kWaitLimitNs) {}
@@ -670,6 +664,37 @@ chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ Pag
         if (q_issued > 0) {
           const unsigned long long w0 = globaltimer_ns();
           while (!mbar_try_wait(&bars->q_full, (uint32_t)(q_issued - 1) & 1u) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+        }
+      }
+    }
+    __syncwarp();
+  } else if (PAIR && warp == 1 && !leader) {
+    // ------------------------------------------------------------ arrivals of the odd CTA's loads
+    // Every CTA's copies complete on its own barriers, and this thread passes the odd CTA's on to the
+    // even one, which issues the MMAs. (Copies that complete on the other CTA's barrier,
+    // cta_group::2, take 4,000 to 6,000 cycles each and 4.1 TB/s together with 96 KB in flight
+    // per SM; on the own one 900 to 1,900 cycles and 10 TB/s.)
+    if (elect_one()) {
+      auto pass = [&](uint64_t* bar, uint32_t parity) -> bool {
+        if (!mbar_wait(bar, parity, abort_flag)) return false;
+        fence_proxy_async_smem();
+        mbar_arrive_cluster(smem_u32(bar) & kPeerBitMask);
+        return true;
+      };
+      int st = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      int unit_iter = 0;
+      for (int r = 0; r < nrounds && ok; ++r) {
+        Unit w;
+        if (!unit_of_round(r, w)) continue;
+        if (w.ntiles == 0) continue;
+        ok = pass(&bars->q_full, (uint32_t)unit_iter & 1u);
+        ++unit_iter;
+#pragma unroll 1
+        for (int s = 0; s < w.ntiles * (Cfg::kKStages + Cfg::kVStages) && ok; ++s) {
+          ok = pass(&bars->ring_full[st], ph);
+          if (++st == Cfg::kStages) { st = 0; ph ^= 1u; }
         }
       }
     }
