@@ -154,6 +154,7 @@ struct PagedRowsShape {
   int unit_rows, row_groups;
   int cut;                  // units are cut into equal runs
   int parts;                // places for parts of cut units
+  long long line;           // most blocks of all units together
   // row-group kernel (paged_decode.cu)
   int warp_teams;           // units go to single warps, not CTAs
   int q_rows;               // rows of the fullest group

@@ -80,6 +80,7 @@ int attend_plan(const gemma_attn_params* p, bool e4m3, int batch, int total_q, i
   L->chunk = (long long)max_q * group > kChunkMinRows;
   const int r = rotated_pairs(p->rope_p, d);
   L->shape = paged_rows_shape(d, local, r, batch, hkv, L->chunk ? kChunkMinRows : std::max(1, max_q * group), keys);
+  if (L->shape.line > 0x7fffffffll) return GEMMA_ATTN_ERR_UNSUPPORTED;
   if (L->shape.cut) {
     L->part_o = take((size_t)L->shape.parts * L->shape.unit_rows * d * 4);
     L->part_lse = take((size_t)L->shape.parts * L->shape.unit_rows * 4);

@@ -402,6 +402,8 @@ int gemma_attn_paged_workspace_size(const gemma_attn_params* params, const gemma
  *   max_q, max_cache_len  upper bounds of a sequence's new tokens and of cache_seqlens. A
  *             sequence beyond either, or past max_blocks * page_size, records
  *             GEMMA_ATTN_ERR_SEQLEN and its rows are not written.
+ *             batch * num_kv_heads * (groups of 8 or 40 rows) * (visible keys / 64; 16 for 64 dims, or
+ *             more than 64 rotated pairs) must stay under 2^31 (GEMMA_ATTN_ERR_UNSUPPORTED).
  *   workspace device buffer of gemma_attn_paged_workspace_size() bytes, 256-byte aligned;
  *             contents are scratch, nothing in it needs clearing. For long chunks it holds
  *             16-bit copies of what the tensor cores cannot read from the pages (GLOBAL: the
