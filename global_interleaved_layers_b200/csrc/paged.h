@@ -175,7 +175,7 @@ struct ChunkPlan {
   int* unit0;               // [batch + 1]: first unit
   int4* list;               // pairs {sequence, unit of it, first key tile, end}, {partial slot or -1, -, -, -}
   int4* merges;             // {sequence, unit of it, first slot, pieces}
-  uint16_t* q_side;         // [T, Hq, q_cols] rotated 64-dim chunks of the queries
+  uint16_t* q_side;         // [T, Hq, q_cols (twice with q_lo)] rotated 64-dim chunks of the queries
   uint16_t* k_rot;          // [Hkv, rot_rows, k_cols] rotated chunks of K=V keys, every tile
   uint16_t* k_copy;         // [Hkv, copy_rows, d] bf16 rows of every tile (e4m3) or of the cut ones (bf16)
   uint16_t* v_copy;
@@ -183,6 +183,7 @@ struct ChunkPlan {
   float* part_lse;          // [slots, Hkv, rows]
   uint32_t q_mask, k_mask;  // 64-dim chunks that come from q_side / k_rot
   int q_cols, k_cols;
+  int q_lo;                 // rotated queries in two bf16 parts (ChunkCfg)
   long long rot_rows, copy_rows;
   int e4m3;
   int min_rows;             // sequences with more rows per KV head than this are chunks

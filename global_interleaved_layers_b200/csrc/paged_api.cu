@@ -57,6 +57,7 @@ struct AttendPlan {
   bool pair;
   int tokens, units_x, clusters, slots, units, seqs;
   uint32_t q_mask, k_mask;
+  bool q_lo;                        // rotated queries in two bf16 parts
   long long tiles, copy_rows;
   size_t header, chunk_of, tile0, unit0, list, merges, q_side, k_rot, k_copy, v_copy, c_part_o, c_part_lse;
   size_t total;
@@ -89,6 +90,7 @@ int attend_plan(const gemma_attn_params* p, bool e4m3, int batch, int total_q, i
   if (L->chunk) {
     L->q_mask = rotated_chunk_mask(d, r);
     L->k_mask = local ? 0u : L->q_mask;
+    L->q_lo = local && d <= 256 && L->q_mask != 0;
     L->pair = d >= 128 && (long long)max_q * group > 128;
     L->tokens = 128 / group * (L->pair ? 2 : 1);
     L->units_x = hkv * (d > 256 ? d / 256 : 1);
@@ -110,7 +112,7 @@ int attend_plan(const gemma_attn_params* p, bool e4m3, int batch, int total_q, i
     L->unit0 = take(((size_t)batch + 1) * 4);
     L->list = take((size_t)(L->units + L->slots) * 32);
     L->merges = take((size_t)L->slots * 16);
-    L->q_side = take((size_t)rows * __builtin_popcount(L->q_mask) * 128);
+    L->q_side = take((size_t)rows * __builtin_popcount(L->q_mask) * (L->q_lo ? 256 : 128));
     L->k_rot = take((size_t)L->tiles * 128 * hkv * __builtin_popcount(L->k_mask) * 128);
     L->k_copy = take((size_t)L->copy_rows * hkv * d * 2);
     L->v_copy = local ? take((size_t)L->copy_rows * hkv * d * 2) : L->k_copy;
@@ -153,6 +155,7 @@ int launch_attend_chunks(const gemma_attn_params* params, const PagedAttendArgs&
   p.q_mask = L.q_mask;
   p.k_mask = L.k_mask;
   p.q_cols = __builtin_popcount(L.q_mask) * 64;
+  p.q_lo = L.q_lo ? 1 : 0;
   p.k_cols = __builtin_popcount(L.k_mask) * 64;
   p.rot_rows = L.tiles * 128;
   p.copy_rows = L.copy_rows;
@@ -168,7 +171,7 @@ int launch_attend_chunks(const gemma_attn_params* params, const PagedAttendArgs&
   ChunkMaps m;
   bool ok = box_map(&m.q, a.q, d, a.hq, a.total_q, a.group, tpc);
   m.qs = m.q;
-  if (L.q_mask) ok &= box_map(&m.qs, p.q_side, p.q_cols, a.hq, a.total_q, a.group, tpc);
+  if (L.q_mask) ok &= box_map(&m.qs, p.q_side, L.q_lo ? 2 * p.q_cols : p.q_cols, a.hq, a.total_q, a.group, tpc);
   ok &= box_map(&m.k_copy, p.k_copy, d, p.copy_rows, hkv, keys, 1);
   ok &= box_map(&m.v_copy, p.v_copy, d, p.copy_rows, hkv, 128, 1);
   m.k = m.k_copy;

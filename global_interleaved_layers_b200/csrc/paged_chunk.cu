@@ -44,13 +44,18 @@ constexpr int kCChunkBytes = 16384;          // 128 rows x 64 dims
 constexpr int kCMaxStages = 16;
 constexpr int kCBarBytes = 2048;
 
-template <int D, bool PAIR>
+// LO: the rotated query chunks keep 16 bits, in two bf16 chunks (hi + lo) whose products add up.
+// Rotating makes a bf16 row fp32, and rounding it back would be the largest error of a layer that
+// rotates every dim (with the weights' rounding, relative to the outputs 2.1e-3 against 1.1e-3).
+// Sliding-window layers have it up to 256 dims; at 512 the second copy does not fit, and
+// K=V layers' keys are rounded after the same rotation anyway, of a quarter of the dims.
+template <int D, bool PAIR, bool LO>
 struct ChunkCfg {
   static constexpr int kDv = D > 256 ? 256 : D;               // output columns per unit
   static constexpr int kParts = D / kDv;
   static constexpr int kQChunks = D / 64;
   static constexpr int kVChunks = kDv / 64;
-  static constexpr int kQBytes = kQChunks * kCChunkBytes;
+  static constexpr int kQBytes = (LO ? 2 : 1) * kQChunks * kCChunkBytes;
   // Single: a stage is one 64-dim chunk of 128 keys (K) or one 64-column chunk (V). Pair at
   // d >= 256: four chunks of the CTA's 64 keys, or two column chunks of 128 keys; at 128: half.
   static constexpr int kStageBytes = (PAIR && D >= 256) ? 2 * kCChunkBytes : kCChunkBytes;
@@ -318,9 +323,22 @@ __global__ void __launch_bounds__(kSideThreads) chunk_side_kernel(PagedAttendArg
           bf8_to_f32(w0[k], x0);
           bf8_to_f32(w1[k], x1);
           turn8(x0, x1, c, s, y0, y1);
-          uint16_t* dst = p.q_side + (row + k) * p.q_cols;
-          if (c0 >= 0) *reinterpret_cast<uint4*>(dst + c0) = f32_to_bf8(y0);
-          if (c1 >= 0) *reinterpret_cast<uint4*>(dst + c1) = f32_to_bf8(y1);
+          uint16_t* dst = p.q_side + (row + k) * (p.q_lo ? 2 * p.q_cols : p.q_cols);
+          const uint4 hi0 = f32_to_bf8(y0), hi1 = f32_to_bf8(y1);
+          if (c0 >= 0) *reinterpret_cast<uint4*>(dst + c0) = hi0;
+          if (c1 >= 0) *reinterpret_cast<uint4*>(dst + c1) = hi1;
+          if (!p.q_lo) continue;
+          // what the rounding left; nothing beside an infinity, which says all
+          float h0[8], h1[8];
+          bf8_to_f32(hi0, h0);
+          bf8_to_f32(hi1, h1);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            y0[e] = fabsf(h0[e]) < INFINITY ? y0[e] - h0[e] : 0.f;
+            y1[e] = fabsf(h1[e]) < INFINITY ? y1[e] - h1[e] : 0.f;
+          }
+          if (c0 >= 0) *reinterpret_cast<uint4*>(dst + p.q_cols + c0) = f32_to_bf8(y0);
+          if (c1 >= 0) *reinterpret_cast<uint4*>(dst + p.q_cols + c1) = f32_to_bf8(y1);
         }
       }
       continue;
@@ -433,11 +451,11 @@ __global__ void __launch_bounds__(kSideThreads) chunk_side_kernel(PagedAttendArg
 // ---------------------------------------------------------------------------
 // The attention kernel.
 // ---------------------------------------------------------------------------
-template <int D, bool PAIR>
+template <int D, bool PAIR, bool LO>
 __global__ void __launch_bounds__(kCThreads, 1)
 chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ PagedAttendArgs a,
              const __grid_constant__ ChunkPlan p) {
-  using Cfg = ChunkCfg<D, PAIR>;
+  using Cfg = ChunkCfg<D, PAIR, LO>;
   follow();
   if (__ldcg(p.header) == 0) return;
   extern __shared__ uint8_t smem_raw[];
@@ -544,12 +562,15 @@ chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ Pag
           ok = mbar_wait(&bars->q_empty, (uint32_t)(unit_iter - 1) & 1u, abort_flag);
           if (!ok) break;
         }
-        mbar_arrive_expect_tx(&bars->q_full, Cfg::kQChunks * 128u * (uint32_t)(tpc * a.group));
+        mbar_arrive_expect_tx(&bars->q_full, (Cfg::kQChunks + (LO ? __popc(p.q_mask) : 0)) * 128u * (uint32_t)(tpc * a.group));
 #pragma unroll 1
         for (int c = 0; c < Cfg::kQChunks; ++c) {
           const bool rot = (p.q_mask >> c) & 1u;
           load(q_smem + c * kCChunkBytes, rot ? &maps.qs : &maps.q, &bars->q_full, rot ? col_of(p.q_mask, c) : c * 64,
                w.kvh * a.group, w.tok0 + w.t0 + (int)rank * tpc);
+          if (LO && rot)
+            load(q_smem + (Cfg::kQChunks + c) * kCChunkBytes, &maps.qs, &bars->q_full, p.q_cols + col_of(p.q_mask, c), w.kvh * a.group,
+                 w.tok0 + w.t0 + (int)rank * tpc);
         }
         ++q_issued;
         const int first = keys_first(a, w.len, 0), end = w.len + w.n, seq_kt0 = first / kCN;
@@ -745,6 +766,14 @@ chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ Pag
                 for (int kk = 0; kk < 4; ++kk) {
                   if constexpr (PAIR) umma_ss_pair(tmem + s_col, qd + 2 * kk, kds + 2 * kk, idesc_qk, (c | kk) != 0);
                   else umma_ss(tmem + s_col, qd + 2 * kk, kds + 2 * kk, idesc_qk, (c | kk) != 0);
+                }
+                if (LO && ((p.q_mask >> c) & 1u)) {
+                  const uint64_t qlo = qd + (uint64_t)((Cfg::kQChunks * kCChunkBytes) >> 4);
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk) {
+                    if constexpr (PAIR) umma_ss_pair(tmem + s_col, qlo + 2 * kk, kds + 2 * kk, idesc_qk, true);
+                    else umma_ss(tmem + s_col, qlo + 2 * kk, kds + 2 * kk, idesc_qk, true);
+                  }
                 }
               }
               commit_both(&bars->ring_empty[st]);
@@ -1055,12 +1084,12 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(PagedAttendArgs a, Chu
   }
 }
 
-template <int D, bool PAIR>
+template <int D, bool PAIR, bool LO>
 static cudaError_t launch_chunk_t(const ChunkMaps& maps, const PagedAttendArgs& a, const ChunkPlan& p, int units_bound,
                                   cudaStream_t stream) {
-  using Cfg = ChunkCfg<D, PAIR>;
+  using Cfg = ChunkCfg<D, PAIR, LO>;
   static std::atomic<bool> ready[64];
-  const cudaError_t e = allow_smem(chunk_kernel<D, PAIR>, Cfg::kSmemBytes, ready);
+  const cudaError_t e = allow_smem(chunk_kernel<D, PAIR, LO>, Cfg::kSmemBytes, ready);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kCThreads);
@@ -1077,7 +1106,15 @@ static cudaError_t launch_chunk_t(const ChunkMaps& maps, const PagedAttendArgs& 
   cfg.numAttrs = PAIR ? 2 : 1;
   const int clusters = p.clusters < units_bound ? p.clusters : units_bound;
   cfg.gridDim = dim3((unsigned)(clusters * (PAIR ? 2 : 1)));
-  return cudaLaunchKernelEx(&cfg, chunk_kernel<D, PAIR>, maps, a, p);
+  return cudaLaunchKernelEx(&cfg, chunk_kernel<D, PAIR, LO>, maps, a, p);
+}
+
+template <int D>
+static cudaError_t launch_chunk_d(bool pair, const ChunkMaps& maps, const PagedAttendArgs& a, const ChunkPlan& p, int units_bound,
+                                  cudaStream_t stream) {
+  if (p.q_lo)
+    return pair ? launch_chunk_t<D, true, true>(maps, a, p, units_bound, stream) : launch_chunk_t<D, false, true>(maps, a, p, units_bound, stream);
+  return pair ? launch_chunk_t<D, true, false>(maps, a, p, units_bound, stream) : launch_chunk_t<D, false, false>(maps, a, p, units_bound, stream);
 }
 
 cudaError_t launch_chunk(const ChunkMaps& maps, const PagedAttendArgs& a, const ChunkPlan& p, int units_bound,
@@ -1088,10 +1125,14 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const PagedAttendArgs& a, const 
   if (e != cudaSuccess) return e;
   const bool pair = p.rows > kCM;
   switch (a.c.d) {
-    case 64: e = launch_chunk_t<64, false>(maps, a, p, units_bound, stream); break;
-    case 128: e = pair ? launch_chunk_t<128, true>(maps, a, p, units_bound, stream) : launch_chunk_t<128, false>(maps, a, p, units_bound, stream); break;
-    case 256: e = pair ? launch_chunk_t<256, true>(maps, a, p, units_bound, stream) : launch_chunk_t<256, false>(maps, a, p, units_bound, stream); break;
-    case 512: e = pair ? launch_chunk_t<512, true>(maps, a, p, units_bound, stream) : launch_chunk_t<512, false>(maps, a, p, units_bound, stream); break;
+    case 64:
+      e = p.q_lo ? launch_chunk_t<64, false, true>(maps, a, p, units_bound, stream) : launch_chunk_t<64, false, false>(maps, a, p, units_bound, stream);
+      break;
+    case 128: e = launch_chunk_d<128>(pair, maps, a, p, units_bound, stream); break;
+    case 256: e = launch_chunk_d<256>(pair, maps, a, p, units_bound, stream); break;
+    case 512:
+      e = pair ? launch_chunk_t<512, true, false>(maps, a, p, units_bound, stream) : launch_chunk_t<512, false, false>(maps, a, p, units_bound, stream);
+      break;
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
