@@ -28,8 +28,12 @@
 // and loads half of every K and V stage, halving the bytes per product. At head dim 512 a unit
 // accumulates 256 of the output columns (a 128 x 512 fp32 tile would fill TMEM) and the scores
 // are computed by both halves.
-// Bound: the tensor pipe for long chunks (scores once more at d = 512); launch and copy latency
-// for short ones.
+// Bound: the tensor pipe for long chunks (scores once more at d = 512); launches and the units' ends
+// for short ones. Measured: 2,048 tokens after 29,777, K=V of 512 dims, 32 heads: 4.24 ms in a
+// burst (974 TFLOP/s of the visible pairs, 1,460 as executed), 4.85 ms with the clocks that
+// repeated calls settle at; three prompts of 700 to 2,100 tokens on a window of 1,024, 256 dims,
+// 180 us, of which the side copies take 25, the plan 8, the attention 140 (a unit is ten tiles:
+// its fill and its epilogue are a third of it).
 #include "paged.h"
 #include "tile_plan.h"
 

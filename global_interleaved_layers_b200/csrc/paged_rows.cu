@@ -16,6 +16,10 @@
 // a lane and head in two runs of 8 that hold both members of 8 pairs; the heads share the row's
 // place and angles and have their loads in flight together, and a maximum is a shuffle within
 // the group. Whole warps are filled for every head dim.
+// Measured (cold L2): append and gather of a decode step, 64 sequences x 16 KV heads x 256 dims, K
+// and V, e4m3: 8 and 6 us; of 1,000 to 8,191 tokens of six sequences, K=V of 4 x 512: 20 and 17 us
+// (4.6 and 5.4 TB/s); gather of three whole sequences, 53k tokens of 16 x 256, 205 us (5.5 TB/s).
+// A head at a time (the loads of one in flight) the last two took 43 and 233 us.
 #include "paged.h"
 
 namespace gattn {

@@ -12,9 +12,9 @@
 //
 // E4M3 pages are not widened at all: codes go into kind::f8f6f4 MMAs. The other operand is 16-bit
 // information split into two e4m3 columns whose sum it is, x = hi + lo with hi = rn(x) and
-// lo = rn(x - hi): each takes 4 bits, so the pair holds 8, the bits of a bf16 (a bf16 query
-// element is held exactly down to 2^-9; a weight is rounded by at most 2^-8 of itself, as
-// rounding it to bf16 would). N is twice the rows, and with N's granularity of 16 the second
+// lo = rn(x - hi): each takes 4 bits, so the pair holds 8, the bits of a bf16 (a rotated query
+// element, which is split from fp32, and a weight are off by at most 2^-8 of themselves, as
+// rounding them to bf16 would leave them). N is twice the rows, and with N's granularity of 16 the second
 // half of 8 rows is free. Query rows are scaled by a power of two to a largest magnitude in
 // [128, 256), weights to at most 448. The rotated dims are fp16 (codes turned in fp32, one
 // rounding of 2^-11) in kind::f16 MMAs on the same accumulator. A key's scale multiplies its
@@ -28,17 +28,27 @@
 // units, the next unit's query rows are prepared and its first tiles loaded and scored while
 // the last one's products and output finish.
 //
-// Roles (512 threads): warp 0 loads (TMA, one box per page and 128-byte column chunk, a whole
-// tile's boxes back to back so that a row's columns are asked for together); warp 1 owns TMEM
-// and issues the score MMAs, a tile ahead; warp 2 issues the value MMAs; warp 3 clears the rows
-// of a sequence's first and last tile that no query sees (pages may hold anything there, NaN
-// included); the next eight warps (four when the rows take two softmax groups) prepare query
-// rows and turn K=V chunks; the last one or two groups of four warps run the softmax: a thread
-// owns a key (its TMEM lane) and up to 20 rows. The running maxima are only raised when a score
-// passes them by more than the weights' headroom; until then a tile costs each warp one vote and
-// one meeting of four warps, no reduction.
+// Roles (512 threads): warp 0 loads (TMA; a ring slot is 16 KB, one 128-byte column chunk of 128
+// keys or two of 64, so that a page as long as the tile is one copy); warp 1 owns TMEM and issues
+// the score MMAs, a tile ahead; warp 2 issues the value MMAs; warp 3 hands out the CTA's runs,
+// four ahead, and clears the rows of a sequence's first and last tile that no query sees (pages
+// may hold anything there, NaN included); warps 4-7 prepare query rows and turn K=V chunks; warps
+// 8-15 are two softmax groups, a thread owning a key (its TMEM lane) and 8 or 20 rows. For units
+// of 8 rows the groups take every other tile, each with references, sums and an output of its
+// own, joined at the unit's end; for 40 rows each has half of them. The references are only
+// raised when a score passes them by more than the weights' headroom; until then a tile costs
+// each warp one vote and one meeting of four warps, no reduction.
 // Every wait is bounded: one that runs out records a timeout and the CTA unwinds.
-// Bound: HBM, each visible row read once.
+//
+// Bound: HBM, each visible row read once. Measured (cold L2): 8 sequences of 30k to 32k keys, 512
+// dims, bf16, 188 us with the join (5.4 TB/s; the loads' share of HBM is 24 B a cycle and SM,
+// a 64 KB tile takes 3,000 cycles of the 2,700 that allows); 64 sequences on a window of 1,024,
+// 256 dims, e4m3, 136 us (3.7 TB/s: a unit is nine tiles, and its first scores and its output
+// leave gaps); 40 rows of 16 sequences against 1k to 32k keys, 512 dims, e4m3, 128 us: there the ring
+// holds not two tiles beside the query rows' and weights' two columns each, and a tile's chain
+// (load, rotation, scores, weights, values) of 10,000 cycles bounds it.
+// Instruction fetch and the latency of single warps count as much as bytes here: the first form,
+// with a lane per box and waits in every role's loop, took 506 and 400 us of the first and third.
 #include <algorithm>
 
 #include "paged.h"
@@ -77,16 +87,19 @@ struct __align__(16) TileHeader {
   float sums[2][2][4][H <= 8 ? 8 : 32];    // [unit parity][group][quadrant][row]
   float step[2][2][H];      // a group's factors for sums and output when its references move
   float refs[2][2][2][H];   // [unit parity][group]: references of the sums and of the weights
-  float qsc[4][SG * H];         // e4m3: score factor of a unit's rows (unit mod 4)
-  int orow[4][SG * H];          // output row (token x query heads + head) of a unit's rows
-  int qpos[4][SG * H];          // and their positions
+  // Of a unit's rows (unit mod 8: query rows are prepared up to two units ahead of the scores, which
+  // run up to three ahead of the output): score factor (e4m3), output row (token x query heads +
+  // head), position.
+  float qsc[8][SG * H];
+  int orow[8][SG * H];
+  int qpos[8][SG * H];
   TilePiece piece[8];
   double itf[64];           // theta_j / (2 pi), 0 past the rotated pairs
 };
 
 // Shape of a CTA for units of NR = SG * H rows. Two softmax groups: with SG = 2 each has half of
 // the rows, with SG = 1 every other tile (and an output of its own, joined at the end).
-template <int D, bool E4M3, int SG, int H>
+template <int D, bool E4M3, bool SAME, int SG, int H>
 struct TileCfg {
   static constexpr int KT = (!E4M3 && D == 512) ? 64 : 128;   // keys per tile
   static constexpr int NR = SG * H;                           // rows of a unit
@@ -94,21 +107,26 @@ struct TileCfg {
   static constexpr int HW = 4;                                // warps for query rows and rotation
   // columns: the MMA's N, in 16s (8s with 64 keys on M, for the scores: NQ below)
   static constexpr int N = E4M3 ? (2 * NR + 15) / 16 * 16 : (NR + 15) / 16 * 16;
-  static constexpr int LO = NR;                               // first lo column (e4m3)
+  static constexpr int LO = NR;                               // first lo column
+  // Sliding-window layers rotate every dim of a query row, and rounding it back to bf16 would be the
+  // largest error of their outputs (relative 1.8e-3; the weights' rounding 1.1e-3): it stays hi + lo
+  // there too, in bf16 columns. (Not 40 rows of 512 dims, beside which no tile would fit.)
+  static constexpr bool QLO = !E4M3 && !SAME && !(D == 512 && NR > 8);
+  static constexpr int SN = QLO ? (2 * NR + 15) / 16 * 16 : N;  // columns of a score buffer
   static constexpr int CH = E4M3 ? D / 128 : D / 64;          // 128-byte chunks of a row
   static constexpr int PB = D / 128;                          // 128-dim blocks of the output
   static constexpr int CHUNK = KT * 128;                      // bytes of a chunk of a tile
   static constexpr int G = kTSlotBytes / CHUNK;               // chunks of a ring slot
   static constexpr int NS = CH / G;                           // slots of a tile's keys (or values)
   static constexpr int PER = CH / PB / G;                     // slots of a 128-dim block
-  static constexpr int NQ = KT == 64 && NR <= 8 ? 8 : N;      // query rows with padding
+  static constexpr int NQ = QLO ? SN : KT == 64 && NR <= 8 ? 8 : N;  // query rows with padding
   static constexpr int QROT = E4M3 ? 2 * NQ * 128 : 0;        // fp16 rows of the rotated dims
   static constexpr int QB = CH * NQ * 128 + QROT;
   static constexpr int P_B = E4M3 ? N * 128 : KT / 64 * N * 128;
   static constexpr int ROT = 2 * KT * 128;                    // two chunks of 64 dims, 16 bits
   static constexpr int HEADER = (sizeof(TileHeader<SG, H>) + 1023) / 1024 * 1024;
   static constexpr int BUDGET = 232448 - 1024 - HEADER;
-  static constexpr int COL_O = 2 * N;
+  static constexpr int COL_O = 2 * SN;
   static_assert(COL_O + TG * PB * N <= 512, "TMEM columns");
   static_assert(CH % G == 0 && PER >= 1, "slots of a tile");
 };
@@ -123,9 +141,10 @@ struct TileTurns {
 struct TileBufs {
   int nq, nrot, kslots, vslots;  // value ring only for separate values
 };
-template <int D, bool E4M3, int SG, int H>
-__host__ __device__ inline TileBufs tile_bufs(bool kv_same, bool rot) {
-  using C = TileCfg<D, E4M3, SG, H>;
+template <int D, bool E4M3, bool SAME, int SG, int H>
+__host__ __device__ inline TileBufs tile_bufs(bool rot) {
+  using C = TileCfg<D, E4M3, SAME, SG, H>;
+  constexpr bool kv_same = SAME;
   // As much ring as three tiles, then a second buffer for the rotated copy, then one for the
   // next unit's query rows.
   TileBufs b;
@@ -341,7 +360,7 @@ template <int D, bool E4M3, bool SAME, int SG, int H>
 __global__ void __launch_bounds__(kTThreads, 1)
 paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   const __grid_constant__ PagedAttendArgs a, const __grid_constant__ TileTurns turns) {
-  using C = TileCfg<D, E4M3, SG, H>;
+  using C = TileCfg<D, E4M3, SAME, SG, H>;
   constexpr int KT = C::KT, N = C::N, NQ = C::NQ, NR = C::NR, CH = C::CH, PB = C::PB, HALF = D / 2;
   constexpr int G = C::G, NS = C::NS, TG = C::TG;
   // slot of a tile that holds the second half's rotated dims (the first holds the first half's)
@@ -354,7 +373,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
   Header* hd = reinterpret_cast<Header*>(base);
   constexpr bool kv_same = SAME;
   const bool rot = SAME && a.r > 0;
-  const TileBufs bufs = tile_bufs<D, E4M3, SG, H>(kv_same, rot);
+  const TileBufs bufs = tile_bufs<D, E4M3, SAME, SG, H>(rot);
   uint8_t* q_s = base + C::HEADER;
   uint8_t* p_s = q_s + bufs.nq * C::QB;
   uint8_t* rot_s = p_s + 2 * C::P_B;
@@ -535,7 +554,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
         const uint32_t q_addr = smem_u32(q_s + qb * C::QB) >> 4, ring_addr = smem_u32(kring) >> 4;
 #pragma unroll 1
         for (int lt = 0; lt < p.ntiles && ok; ++lt, ++t) {
-          const uint32_t sb = tmem + (uint32_t)(t & 1) * N;
+          const uint32_t sb = tmem + (uint32_t)(t & 1) * C::SN;
           // S^T(t) overwrites the scores that softmax(t - 2) read
           if (t >= 2) ok = thread_wait(&hd->p_full[t & 1], (uint32_t)((t - 2) >> 1) & 1u, abort_flag);
           uint32_t acc = 0;
@@ -746,8 +765,8 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
         const int orow = (np.tok0 + tk) * a.hq + np.kvh * a.group + hh;
         const uint16_t* src = a.q + (size_t)orow * D;
         if (lane == 0) {
-          hd->orow[q_piece & 3][row] = orow;
-          hd->qpos[q_piece & 3][row] = np.len + tk;
+          hd->orow[q_piece & 7][row] = orow;
+          hd->qpos[q_piece & 7][row] = np.len + tk;
         }
         uint32_t w0[QI], w1[QI];
 #pragma unroll
@@ -771,16 +790,25 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
             }
           }
         }
+        // y: the row's elements in fp32, rotated; {first half's two, second half's two}
+        float y[QI][2][2];
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < QI; ++i) {
+          y[i][0][0] = __uint_as_float(w0[i] << 16);
+          y[i][0][1] = __uint_as_float(w0[i] & 0xFFFF0000u);
+          y[i][1][0] = __uint_as_float(w1[i] << 16);
+          y[i][1][1] = __uint_as_float(w1[i] & 0xFFFF0000u);
           if (have && 64 * i < a.r) {
-            const float x00 = __uint_as_float(w0[i] << 16), x01 = __uint_as_float(w0[i] & 0xFFFF0000u);
-            const float x10 = __uint_as_float(w1[i] << 16), x11 = __uint_as_float(w1[i] & 0xFFFF0000u);
-            w0[i] = pack_bf16x2(x00 * c0[i].x - x10 * c0[i].y, x01 * c1[i].x - x11 * c1[i].y);
-            w1[i] = pack_bf16x2(x00 * c0[i].y + x10 * c0[i].x, x01 * c1[i].y + x11 * c1[i].x);
+            const float x00 = y[i][0][0], x01 = y[i][0][1], x10 = y[i][1][0], x11 = y[i][1][1];
+            y[i][0][0] = x00 * c0[i].x - x10 * c0[i].y;
+            y[i][0][1] = x01 * c1[i].x - x11 * c1[i].y;
+            y[i][1][0] = x00 * c0[i].y + x10 * c0[i].x;
+            y[i][1][1] = x01 * c1[i].y + x11 * c1[i].x;
           }
-          if (E4M3) top = max(max(top, max((w0[i] & 0x7FFFu) << 16, w0[i] & 0x7FFF0000u)), max((w1[i] & 0x7FFFu) << 16, w1[i] & 0x7FFF0000u));
+          if (E4M3)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(y[i][e >> 1][e & 1]) & 0x7FFFFFFFu);
         }
         float up = 1.f;
         if constexpr (E4M3) {
@@ -792,7 +820,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
           const int k = top == 0u || E == 255 ? 0 : min(max(134 - E, -126), 126);
           up = __uint_as_float((uint32_t)(127 + k) << 23);
           if (lane == 0)
-            hd->qsc[q_piece & 3][row] =
+            hd->qsc[q_piece & 7][row] =
                 E == 255 ? __uint_as_float(0x7FC00000u)
                          : a.softmax_scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 - k) << 23);
         }
@@ -802,11 +830,19 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
             const int dim = part * HALF + 64 * i + 2 * lane;
-            const uint32_t w = part ? w1[i] : w0[i];
             if constexpr (!E4M3) {
-              *reinterpret_cast<uint32_t*>(qd + (dim >> 6) * NQ * 128 + sw128(row, (dim & 63) * 2)) = w;
+              const float x0 = y[i][part][0], x1 = y[i][part][1];
+              const uint32_t w = pack_bf16x2(x0, x1);
+              uint8_t* chunk = qd + (dim >> 6) * NQ * 128;
+              *reinterpret_cast<uint32_t*>(chunk + sw128(row, (dim & 63) * 2)) = w;
+              if (C::QLO && 64 * i < a.r) {
+                // what the rounding left; nothing beside an infinity, which says all
+                const float h0 = __uint_as_float(w << 16), h1 = __uint_as_float(w & 0xFFFF0000u);
+                *reinterpret_cast<uint32_t*>(chunk + sw128(C::LO + row, (dim & 63) * 2)) =
+                    pack_bf16x2(fabsf(h0) < INFINITY ? x0 - h0 : 0.f, fabsf(h1) < INFINITY ? x1 - h1 : 0.f);
+              }
             } else {
-              const float x0 = __uint_as_float(w << 16) * up, x1 = __uint_as_float(w & 0xFFFF0000u) * up;
+              const float x0 = y[i][part][0] * up, x1 = y[i][part][1] * up;
               const uint32_t hi = e4m3x2(x0, x1);
               const float2 h = unpack_f16x2(e4m3_lo(hi));
               uint8_t* chunk = qd + (dim >> 7) * NQ * 128;
@@ -1005,27 +1041,35 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
         tc_fence_after();
         // sv: scores in log2 units; lv: log2 of the value scale, a power of two (NaN stays NaN)
         float sv[H], lv = 0.f;
-        tmem_ld_n<H>(lane_tmem + bb * N, reinterpret_cast<uint32_t*>(sv));
+        tmem_ld_n<H>(lane_tmem + bb * C::SN, reinterpret_cast<uint32_t*>(sv));
         if constexpr (E4M3) {
           lv = vscale == vscale ? (float)((int)(__float_as_uint(vscale) >> 23) - 127) : vscale;
           float s2[H];
-          tmem_ld_n<H>(lane_tmem + bb * N + C::LO, reinterpret_cast<uint32_t*>(s2));
+          tmem_ld_n<H>(lane_tmem + bb * C::SN + C::LO, reinterpret_cast<uint32_t*>(s2));
           tmem_ld_wait();
-          const float* cf = &hd->qsc[piece & 3][rh];
+          const float* cf = &hd->qsc[piece & 7][rh];
 #pragma unroll
           for (int q = 0; q < H; ++q) sv[q] = (sv[q] + s2[q]) * (cf[q] * kscale);
         } else {
-          tmem_ld_wait();
           const float cf = a.softmax_scale * 1.4426950408889634f;
+          if constexpr (C::QLO) {
+            float s2[H];
+            tmem_ld_n<H>(lane_tmem + bb * C::SN + C::LO, reinterpret_cast<uint32_t*>(s2));
+            tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < H; ++q) sv[q] *= cf;
+            for (int q = 0; q < H; ++q) sv[q] = (sv[q] + s2[q]) * cf;
+          } else {
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < H; ++q) sv[q] *= cf;
+          }
         }
         // tiles that every row sees whole need no mask (rows past the unit's read zero queries)
         if (k0 + KT - 1 > p.len || k0 < p.first || (a.is_local && k0 < p.end - a.window) || !key_lane) {
           const int pos = key_lane ? k0 + u : 0x7fffffff;
 #pragma unroll
           for (int q = 0; q < H; ++q) {
-            const int qp = hd->qpos[piece & 3][rh + q];
+            const int qp = hd->qpos[piece & 7][rh + q];
             if (pos > qp || (a.is_local && pos <= qp - a.window)) sv[q] = -INFINITY;
           }
         }
@@ -1194,7 +1238,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
           sum += l[g] * fac[g];
         }
         const int row = rh + lane;
-        place = p.slot >= 0 ? p.slot * NR + row : hd->orow[piece & 3][row];
+        place = p.slot >= 0 ? p.slot * NR + row : hd->orow[piece & 7][row];
         const float inv = sum > 0.f ? __fdividef(1.f, sum) : sum == 0.f ? 0.f : sum;  // a NaN sum stays one
 #pragma unroll
         for (int g = 0; g < TG; ++g) {
@@ -1286,8 +1330,8 @@ static const TileTurns& tile_turns(int d, double log2_base) {
 
 template <int D, bool E4M3, bool SAME, int SG, int H>
 static cudaError_t launch_tile_t(PagedAttendArgs a, bool cut, long long units, cudaStream_t stream) {
-  using C = TileCfg<D, E4M3, SG, H>;
-  const TileBufs b = tile_bufs<D, E4M3, SG, H>(SAME, SAME && a.r > 0);
+  using C = TileCfg<D, E4M3, SAME, SG, H>;
+  const TileBufs b = tile_bufs<D, E4M3, SAME, SG, H>(SAME && a.r > 0);
   if (b.kslots < C::NS || (!SAME && b.vslots < C::NS)) return cudaErrorInvalidValue;
   static std::atomic<bool> ready[64];
   cudaError_t e = allow_smem(paged_tile_kernel<D, E4M3, SAME, SG, H>, 232448, ready);
