@@ -1141,7 +1141,7 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const PagedAttendArgs& a, const 
   }
   if (e != cudaSuccess) return e;
   // a unit that is cut has two pieces at least; a warp takes up to four rows' columns
-  const dim3 grid((unsigned)(slots / 2), (unsigned)a.c.hkv, (unsigned)((p.rows * ((a.c.d + 127) / 128) + 31) / 32));
+  const dim3 grid((unsigned)((slots + 1) / 2), (unsigned)a.c.hkv, (unsigned)((p.rows * ((a.c.d + 127) / 128) + 31) / 32));
   return launch_follower(chunk_merge_kernel, grid, dim3(256), 0, stream, a, p);
 }
 

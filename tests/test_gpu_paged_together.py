@@ -192,3 +192,9 @@ def test_a_race_of_neighbouring_quotients():
     G.gemma_attn_draft_verify(torch.tensor(p).view(B, 1, V).cuda(), None, torch.zeros(B, 0, dtype=torch.int32, device="cuda"), None,
                               torch.zeros(B, 0, device="cuda"), torch.tensor(e).cuda(), acc, out)
     assert acc.tolist() == [0] * B and out[:, 0].tolist() == want.tolist()
+
+
+def test_more_kv_heads_than_a_plan_cuts_units():
+    # a chunk's units go over all KV heads at once; with this many none may be cut
+    layer = Layer(G.GLOBAL, 600, 600, 64, 0, "bf16", 16, 1, 6, 9)
+    layer.step([70], [0], 70, 0, pad=0)
