@@ -169,9 +169,23 @@ __global__ void __launch_bounds__(kDraftThreads, 2) draft_verify_kernel(DraftArg
         x = __uint_as_float(__reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32)));
       }
     }
+    // The rest: the last few words, or all where a row of an odd vocabulary is not aligned.
+    constexpr int W = 8;
 #pragma unroll 1
-    for (int v = 4 * quads + rank * kDraftThreads + tid; v < a.vocab; v += step)
-      take(prob_at(pt, v, BF16), sub ? prob_at(qt, v, BF16) : 0.f, __ldg(nz + v), v);
+    for (int v0 = 4 * quads + rank * kDraftThreads + warp * 32; v0 < a.vocab; v0 += W * step) {
+      float p[W], q[W], e[W];
+#pragma unroll
+      for (int u = 0; u < W; ++u) {
+        const int v = v0 + u * step + lane;
+        const bool get = v < a.vocab && v >= 0;
+        p[u] = get ? prob_at(pt, v, BF16) : 0.f;
+        e[u] = get ? __ldg(nz + v) : 0.f;
+        q[u] = get && sub ? prob_at(qt, v, BF16) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < W; ++u) take(p[u], q[u], e[u], v0 + u * step + lane);
+      x = __uint_as_float(__reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32)));
+    }
 
     best = shfl_max(best);
     if (lane == 0) s_warp[warp] = best;

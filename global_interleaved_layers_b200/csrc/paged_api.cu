@@ -324,7 +324,7 @@ int gemma_attn_draft_verify(const void* target_probs, const void* draft_probs, i
   set_launch_count(0);
   if (prob_dtype != GEMMA_ATTN_PROBS_F32 && prob_dtype != GEMMA_ATTN_PROBS_BF16) return GEMMA_ATTN_ERR_INVALID_ARG;
   if (batch < 0 || max_draft < 0 || vocab < 1) return GEMMA_ATTN_ERR_INVALID_ARG;
-  if (batch > (0x7fffffff / 8) || max_draft > (1 << 20)) return GEMMA_ATTN_ERR_UNSUPPORTED;
+  if (batch > (0x7fffffff / 8) || max_draft > (1 << 20) || vocab > (1 << 30)) return GEMMA_ATTN_ERR_UNSUPPORTED;
   if (batch == 0) return GEMMA_ATTN_OK;
   if (!target_probs || !noise || !num_accepted || !out_tokens) return GEMMA_ATTN_ERR_INVALID_ARG;
   if (max_draft > 0 && (!draft_tokens || !uniforms)) return GEMMA_ATTN_ERR_INVALID_ARG;

@@ -436,6 +436,7 @@ int gemma_attn_paged_attend(const gemma_attn_params* params, const gemma_attn_pa
  *             the unit exponential. Entries of noise that are not positive never win.
  *   num_accepted [batch] int32, written; out_tokens [batch, max_draft + 1] int32, written: the
  *             accepted tokens, the drawn one, then -1.
+ * vocab <= 2^30, max_draft <= 2^20.
  * A drafted token outside [0, vocab) is never accepted. A draft_lens entry outside
  * [0, max_draft] is brought into that range and records GEMMA_ATTN_ERR_SEQLEN.
  */

@@ -1,4 +1,6 @@
 """Limits and names of the paged-cache entry points that need no GPU."""
+import ctypes
+
 import pytest
 
 G = pytest.importorskip("global_interleaved_layers_b200")
@@ -21,3 +23,9 @@ def test_a_batch_with_too_many_blocks_of_keys_is_refused(kind, d, hkv):
         G.gemma_attn_paged_workspace_size(p, cache, 60000, 60000, 1, keys)
     assert e.value.status == G.ERR_UNSUPPORTED
     assert G.gemma_attn_paged_workspace_size(p, cache, 60000, 60000, 1, keys // 4) > 0
+
+
+def test_vocabularies_past_the_index_range_are_refused():
+    f = 1 << 20  # never dereferenced: the check comes first
+    args = [f, f, G.PROBS_F32, f, ctypes.c_void_p(None), f, f, 2, 3, (1 << 30) + 1, f, f, 0]
+    assert G.raw_call("gemma_attn_draft_verify", *args) == G.ERR_UNSUPPORTED
