@@ -134,12 +134,12 @@ struct PagedAttendArgs {
   int r;                    // rotated pairs
   double log2_base;
   float softmax_scale;
-  // row-group kernel: parts of cut units, two a team
-  float* partial_o;         // [2 teams, 8, d]
-  float* partial_lse;       // [2 teams, 8]
+  // short sequences: parts of cut units, two a team
+  float* partial_o;         // [2 teams, unit_rows, d]
+  float* partial_lse;       // [2 teams, unit_rows]
   int4* joins;              // [teams]: the unit that a team's run begins and does not end (paged_merge_kernel)
   const int* rest;          // beside chunk_of: sequences with rows that are not chunks
-  int row_groups;           // most groups of 8 rows (query, head of the KV head's group) of a sequence
+  int row_groups;           // most units of one KV head of a sequence
   const int* chunk_of;      // [batch], >= 0: the sequence is chunk_kernel's; null: there are none
   // set at the launch: units are cut into equal runs; teams; a run is a multiple of run_step;
   // rows of a unit (8 or 40), log2 of the keys of a block
