@@ -11,13 +11,20 @@
 // turned into a side buffer that only the scores read.
 //
 // E4M3 pages are not widened at all: codes go into kind::f8f6f4 MMAs. The other operand is 16-bit
-// information split into two e4m3 columns whose sum it is, x = hi + lo with hi = rn(x) and
-// lo = rn(x - hi): each takes 4 bits, so the pair holds 8, the bits of a bf16 (a rotated query
-// element, which is split from fp32, and a weight are off by at most 2^-8 of themselves, as
-// rounding them to bf16 would leave them). N is twice the rows, and with N's granularity of 16 the second
-// half of 8 rows is free. Query rows are scaled by a power of two to a largest magnitude in
-// [128, 256), weights to at most 448. The rotated dims are fp16 (codes turned in fp32, one
-// rounding of 2^-11) in kind::f16 MMAs on the same accumulator. A key's scale multiplies its
+// information split into two e4m3 columns, x = hi + lo / 16 with hi = rn(x) and lo = rn(16 (x - hi));
+// a column has accumulators of its own, so the factor is taken back in fp32. Query rows are scaled
+// by a power of two to a largest magnitude in [128, 256), weights to at most 2^8.75: 16 (x - hi) is
+// then 256 at most. hi and lo take 4 bits each, 8 together, down to e4m3's fixed step at the bottom,
+// 2^-9 (2^-13 in lo): an element is off by at most 2^-8 of itself (as rounding it to bf16 would
+// leave it) or 2^-14, whichever is more, 2^-21 of the row's largest. For a query element that is
+// the end of it. A softmax row may have a hundred thousand weights of that size, equal ones
+// among them whose errors would add up (flat tail at 2^-19.4 of the largest, 131,072 keys: 3 percent
+// of the output; without the factor of 16, 9), so a weight's lo is rounded with a dither: half a
+// step times a number in [-1, 1) that goes through the key positions by the golden ratio. It leaves
+// a weight off by up to 2^-13, without bias, and neighbours' errors cancel (the same tail: 1.4e-4 by
+// arithmetic, 6e-4 measured, of fp32's own additions; weights that are zero stay zero). N is twice the rows, and with N's granularity of 16 the second
+// half of 8 rows is free. The rotated dims are fp16 (codes turned in fp32, one
+// rounding of 2^-11) in kind::f16 MMAs on hi's accumulators. A key's scale multiplies its
 // scores; a value's scale 2^k is folded into its weight: with e = s + k in log2 units, the
 // weight is 2^(e - mv + 7) for a running mv near max e, and the softmax sum takes 2^(s - m) with
 // an m of its own, so scales of any size only move exponents.
@@ -62,6 +69,7 @@ constexpr int kTSlotBytes = 16384;     // of a ring slot: one 128-byte column ch
 constexpr int kTMaxSlots = 14;
 constexpr float kTop8 = 7.f;           // e4m3: the running maximum's weight is 2^7,
 constexpr float kHeadroom8 = 1.75f;    // others up to 2^8.75 < 448
+constexpr float kLo = 16.f;            // factor of the lo columns
 
 // One unit's run of tiles.
 struct __align__(16) TilePiece {
@@ -847,7 +855,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
               const float2 h = unpack_f16x2(e4m3_lo(hi));
               uint8_t* chunk = qd + (dim >> 7) * NQ * 128;
               *reinterpret_cast<uint16_t*>(chunk + sw128(row, dim & 127)) = (uint16_t)hi;
-              *reinterpret_cast<uint16_t*>(chunk + sw128(C::LO + row, dim & 127)) = (uint16_t)e4m3x2(x0 - h.x, x1 - h.y);
+              *reinterpret_cast<uint16_t*>(chunk + sw128(C::LO + row, dim & 127)) = (uint16_t)e4m3x2(kLo * (x0 - h.x), kLo * (x1 - h.y));
               if (i == 0) *reinterpret_cast<uint32_t*>(qd + (CH + part) * NQ * 128 + sw128(row, 4 * lane)) = pack_f16x2(x0, x1);
             }
           }
@@ -1049,7 +1057,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
           tmem_ld_wait();
           const float* cf = &hd->qsc[piece & 7][rh];
 #pragma unroll
-          for (int q = 0; q < H; ++q) sv[q] = (sv[q] + s2[q]) * (cf[q] * kscale);
+          for (int q = 0; q < H; ++q) sv[q] = fmaf(s2[q], 1.f / kLo, sv[q]) * (cf[q] * kscale);
         } else {
           const float cf = a.softmax_scale * 1.4426950408889634f;
           if constexpr (C::QLO) {
@@ -1157,6 +1165,8 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
         }
         const uint32_t pb = p_mine + bb * C::P_B;
         if constexpr (E4M3) {
+          // lo's dither, by the key's position: [-1/2, 1/2) of its smallest step, 2^-9
+          const float dither = (float)(int)((uint32_t)(k0 + u) * 2654435769u) * 0x1p-41f;
 #pragma unroll
           for (int q = 0; q < H; q += 2) {
             l_acc[q] += fast_exp2(sv[q] - m_run[q]);
@@ -1164,7 +1174,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
             const float w0 = fast_exp2(sv[q] + lv - mv_run[q]), w1 = fast_exp2(sv[q + 1] + lv - mv_run[q + 1]);
             const uint32_t hi = e4m3x2(w0, w1);
             const float2 h = unpack_f16x2(e4m3_lo(hi));
-            const uint32_t lo = e4m3x2(w0 - h.x, w1 - h.y);
+            const uint32_t lo = e4m3x2(fmaf(w0 - h.x, kLo, dither), fmaf(w1 - h.y, kLo, dither));
             st_shared_u8(pb + q * 128 + col[q & 7], hi);
             st_shared_u8(pb + (q + 1) * 128 + col[(q + 1) & 7], hi >> 8);
             // LO is a multiple of 8 rows: the same swizzle
@@ -1271,7 +1281,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
           tmem_ld_wait();
 #pragma unroll
           for (int q = 0; q < H; ++q) {
-            const float x = E4M3 ? __uint_as_float(o[q]) + __uint_as_float(o2[q]) : __uint_as_float(o[q]);
+            const float x = E4M3 ? fmaf(__uint_as_float(o2[q]), 1.f / kLo, __uint_as_float(o[q])) : __uint_as_float(o[q]);
             v[q] += x * __shfl_sync(0xffffffffu, fac[g], q);
           }
         }

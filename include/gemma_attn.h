@@ -409,9 +409,12 @@ int gemma_attn_paged_workspace_size(const gemma_attn_params* params, const gemma
  *             16-bit copies of what the tensor cores cannot read from the pages (GLOBAL: the
  *             rotated dims of every key; E4M3: every row), so its size follows max_cache_len. Calls that may run at the
  *             same time (other streams, graphs replayed together) need one each.
- * Keys, probabilities and rotated rows enter the products in 16 bits; scores, softmax
- * statistics and outputs are accumulated in fp32. Over E4M3 pages the result is the attention
- * over the values that gemma_attn_paged_gather reads back.
+ * Keys, probabilities and rotated rows enter the products in 16 bits (bf16 or fp16), or, in
+ * decode and verification over E4M3 pages from 128 head dims on, queries and probabilities as two
+ * 8-bit numbers: a query element off by at most 2^-8 of itself or 2^-21 of its row's largest, a
+ * probability times its value row's scale by 2^-8 of itself or 2^-20 of its row's largest, the
+ * smallest without bias. Scores, softmax statistics and outputs are accumulated in fp32. Over E4M3
+ * pages the values are those that gemma_attn_paged_gather reads back.
  */
 int gemma_attn_paged_attend(const gemma_attn_params* params, const gemma_attn_paged_cache* cache,
                             const void* q, const int32_t* cu_q, const int32_t* cache_seqlens, void* out,
