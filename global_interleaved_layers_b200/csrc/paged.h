@@ -38,6 +38,16 @@ cudaError_t allow_smem(F kernel, int bytes, std::atomic<bool>* ready /* [64] */)
 
 enum : int { kStatusPage = 4 };  // device status word: a block-table entry outside the pool
 
+// A load in a kernel that follows closely (follow(), below): its blocks may be resident while a
+// kernel before it still writes what it is going to read, its predecessors' results in the
+// workspace as well as the call's inputs. The read-only path (__ldg, ld.global.nc) is for data that
+// no one writes while the kernel lives, and the compiler may move such a load over the wait; an
+// ordinary one is ordered by it.
+template <typename T>
+__device__ __forceinline__ T fresh(const T* p) {
+  return *p;
+}
+
 struct PagedCache {
   uint8_t* k;               // [pages, Hkv, page_size, d] bf16 or e4m3
   uint8_t* v;               // null for K=V
@@ -50,7 +60,7 @@ struct PagedCache {
 
 // Page of block `blk` of sequence b, or -1 (recorded) when the entry is outside the pool.
 __device__ __forceinline__ int page_of(const PagedCache& c, int b, int blk) {
-  const int pg = __ldg(c.table + (size_t)b * c.max_blocks + blk);
+  const int pg = fresh(c.table + (size_t)b * c.max_blocks + blk);
   if ((unsigned)pg < (unsigned)c.num_pages) return pg;
   atomicOr(&g_status, kStatusPage);
   return -1;
@@ -66,7 +76,7 @@ __device__ __forceinline__ int seq_of_row(const int32_t* cu, int batch, int t) {
   int lo = 0, hi = batch;  // cu[lo] <= t < cu[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(cu + mid) <= t) lo = mid;
+    if (fresh(cu + mid) <= t) lo = mid;
     else hi = mid;
   }
   return lo;

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PagedAttendArg
   // The workspace is sized for lengths that add up to at most total_q, which seq_ok and
   // prefixes that do not decrease ensure; with one that does, there are no chunks.
   int down = 0;
-  for (int b = tid; b < a.batch; b += kPlanThreads) down |= __ldg(a.cu_q + b + 1) < __ldg(a.cu_q + b);
+  for (int b = tid; b < a.batch; b += kPlanThreads) down |= fresh(a.cu_q + b + 1) < fresh(a.cu_q + b);
   down = __syncthreads_or(down);
   // ---- sequences: chunk index, first side tile, first unit
   int chunks = 0, tiles = 0, units = 0;
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PagedAttendArg
     const int b = b0 + tid;
     int is = 0, nt = 0, nu = 0;
     if (b < a.batch) {
-      const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0, len = __ldg(a.lens + b);
+      const int tok0 = fresh(a.cu_q + b), n = fresh(a.cu_q + b + 1) - tok0, len = fresh(a.lens + b);
       if (n != 0 && !seq_ok(a, tok0, n, len)) {
         atomicOr(&g_status, kStatusSeqlen);
       } else if (!down && n > 0 && (long long)n * a.group > p.min_rows) {
@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PagedAttendArg
     }
     *b = x;
     *qt = u - p.unit0[x];
-    const int n = __ldg(a.cu_q + x + 1) - __ldg(a.cu_q + x), t0 = *qt * p.tokens;
-    chunk_tiles(a, __ldg(a.lens + x), t0, min(t0 + p.tokens, n) - 1, lo, hi);
+    const int n = fresh(a.cu_q + x + 1) - fresh(a.cu_q + x), t0 = *qt * p.tokens;
+    chunk_tiles(a, fresh(a.lens + x), t0, min(t0 + p.tokens, n) - 1, lo, hi);
   };
   unsigned long long mine = 0;
   for (int u = tid; u < units; u += kPlanThreads) {
@@ -304,12 +304,12 @@ __global__ void __launch_bounds__(kSideThreads) chunk_side_kernel(PagedAttendArg
     if (i < nq) {
       const int g = (int)(i % rot_groups), j0 = 8 * g;
       const int h0 = (int)(i / rot_groups % qh) * kSideQHeads, t = (int)(i / rot_groups / qh);
-      if (t >= __ldg(a.cu_q + a.batch) || t < __ldg(a.cu_q)) continue;
+      if (t >= fresh(a.cu_q + a.batch) || t < fresh(a.cu_q)) continue;
       const int b = seq_of_row(a.cu_q, a.batch, t);
       if (p.chunk_of[b] < 0) continue;
       const int c0 = chunk_col(p.q_mask, j0), c1 = chunk_col(p.q_mask, j0 + half);
       float c[8], s[8];
-      angles(__ldg(a.lens + b) + t - __ldg(a.cu_q + b), j0, c, s);
+      angles(fresh(a.lens + b) + t - fresh(a.cu_q + b), j0, c, s);
 #pragma unroll 1
       for (int h = h0; h < min(h0 + kSideQHeads, a.hq); h += kSideHeads) {
         const size_t row = (size_t)t * a.hq + h;
@@ -317,8 +317,8 @@ __global__ void __launch_bounds__(kSideThreads) chunk_side_kernel(PagedAttendArg
 #pragma unroll
         for (int k = 0; k < kSideHeads; ++k) {
           if (h + k >= a.hq) break;
-          w0[k] = __ldg(reinterpret_cast<const uint4*>(a.q + (row + k) * d + j0));
-          w1[k] = __ldg(reinterpret_cast<const uint4*>(a.q + (row + k) * d + j0 + half));
+          w0[k] = fresh(reinterpret_cast<const uint4*>(a.q + (row + k) * d + j0));
+          w1[k] = fresh(reinterpret_cast<const uint4*>(a.q + (row + k) * d + j0 + half));
         }
 #pragma unroll
         for (int k = 0; k < kSideHeads; ++k) {
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kSideThreads) chunk_side_kernel(PagedAttendArg
       }
       kt = tile - p.tile0[b];
     }
-    const int len = __ldg(a.lens + b), end = len + __ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b);
+    const int len = fresh(a.lens + b), end = len + fresh(a.cu_q + b + 1) - fresh(a.cu_q + b);
     const int first = keys_first(a, len, 0);
     kt = edges && (tile & 1) ? (end - 1) / kCN : first / kCN + kt;
     // The copy of the first tile is the first of two, unless it is the last one too.
@@ -391,8 +391,8 @@ __global__ void __launch_bounds__(kSideThreads) chunk_side_kernel(PagedAttendArg
       for (int k = 0; k < kSideHeads; ++k) {
         const uint8_t* at = pool + ((src + k * head_step) * d + j0) * (E4M3 ? 1 : 2);
         const bool get = have && h + k < hkv;
-        w0[k] = get ? __ldg(reinterpret_cast<const Raw*>(at)) : Raw{};
-        w1[k] = get ? __ldg(reinterpret_cast<const Raw*>(at + half * (E4M3 ? 1 : 2))) : Raw{};
+        w0[k] = get ? fresh(reinterpret_cast<const Raw*>(at)) : Raw{};
+        w1[k] = get ? fresh(reinterpret_cast<const Raw*>(at + half * (E4M3 ? 1 : 2))) : Raw{};
       }
     };
     auto widen = [&](Raw w, float scale, float* f) {
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kSideThreads) chunk_side_kernel(PagedAttendArg
         bf8_to_f32(w, f);
       }
     };
-    auto scale_of = [&](const float* scales, int k) { return E4M3 && have && h + k < hkv ? __ldg(scales + src + k * head_step) : 0.f; };
+    auto scale_of = [&](const float* scales, int k) { return E4M3 && have && h + k < hkv ? fresh(scales + src + k * head_step) : 0.f; };
     {
       Raw w0[kSideHeads], w1[kSideHeads];
       float sc[kSideHeads], c[8], s[8];
@@ -484,13 +484,13 @@ chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ Pag
     const int u = r * nclusters + ((r & 1) ? nclusters - 1 - cid : cid);
     if (u >= num_units) return false;
     const int ux = u % p.units_x;
-    const int4 e = __ldg(p.list + 2 * (u / p.units_x)), f = __ldg(p.list + 2 * (u / p.units_x) + 1);
+    const int4 e = __ldcg(p.list + 2 * (u / p.units_x)), f = __ldcg(p.list + 2 * (u / p.units_x) + 1);
     w.b = e.x;
     w.part = ux % Cfg::kParts;
     w.kvh = ux / Cfg::kParts;
-    w.tok0 = __ldg(a.cu_q + e.x);
-    w.n = __ldg(a.cu_q + e.x + 1) - w.tok0;
-    w.len = __ldg(a.lens + e.x);
+    w.tok0 = fresh(a.cu_q + e.x);
+    w.n = fresh(a.cu_q + e.x + 1) - w.tok0;
+    w.len = fresh(a.lens + e.x);
     w.t0 = e.y * p.tokens;
     w.kt_lo = e.z;
     w.ntiles = e.w - e.z;
@@ -593,7 +593,7 @@ chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ Pag
           const bool pages = copy_row(kt) < 0;
 #pragma unroll
           for (int i = 0; i < most; ++i)
-            e[i] = pages && i < count ? __ldg(table + ((kt * kCN + off + i * box) >> a.c.page_shift)) : 0;
+            e[i] = pages && i < count ? fresh(table + ((kt * kCN + off + i * box) >> a.c.page_shift)) : 0;
         };
         // Plane (page, head); a bad page's is past the pool, where a box reads zeros.
         auto plane_of = [&](int e) -> int {
@@ -1041,7 +1041,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(PagedAttendArgs a, Chu
   const int rows = p.rows, tpc = kCM / a.group;          // rows of a unit (128 per CTA), tokens per 128
   const int4 e = __ldcg(p.merges + blockIdx.x);          // sequence, unit, first slot, pieces
   const int kvh = blockIdx.y;
-  const int tok0 = __ldg(a.cu_q + e.x), n = __ldg(a.cu_q + e.x + 1) - tok0;
+  const int tok0 = fresh(a.cu_q + e.x), n = fresh(a.cu_q + e.x + 1) - tok0;
   const size_t head_step = (size_t)a.c.hkv * rows;       // from a piece's part to the next's
 #pragma unroll 1
   for (int i = blockIdx.z * 8 + (threadIdx.x >> 5); i < rows * chunks; i += gridDim.z * 8) {

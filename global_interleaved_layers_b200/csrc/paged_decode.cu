@@ -144,7 +144,7 @@ __device__ __forceinline__ int row_groups_of(int rows, int unit_rows) {
 __device__ __noinline__ void seq_units(const PagedAttendArgs& a, int b, int* blocks, int* units) {
   *blocks = *units = 0;
   if (b >= a.batch) return;
-  const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0, len = __ldg(a.lens + b);
+  const int tok0 = fresh(a.cu_q + b), n = fresh(a.cu_q + b + 1) - tok0, len = fresh(a.lens + b);
   if (n <= 0 || (a.chunk_of && a.chunk_of[b] >= 0) || !seq_ok(a, tok0, n, len)) return;
   *blocks = ((len + n + (1 << a.unit_shift) - 1) >> a.unit_shift) - (keys_first(a, len, 0) >> a.unit_shift);
   *units = min(row_groups_of(n * a.group, a.unit_rows), a.row_groups) * a.c.hkv;
@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
   if (tid == 0) *abort_flag = 0;
   if (a.chunk_of == nullptr && blockIdx.x == 0)    // sequences that are not served are recorded here
     for (int b = tid; b < a.batch; b += NW * 32) {
-      const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0;
-      if (n != 0 && !seq_ok(a, tok0, n, __ldg(a.lens + b))) atomicOr(&g_status, kStatusSeqlen);
+      const int tok0 = fresh(a.cu_q + b), n = fresh(a.cu_q + b + 1) - tok0;
+      if (n != 0 && !seq_ok(a, tok0, n, fresh(a.lens + b))) atomicOr(&g_status, kStatusSeqlen);
     }
   // per pair: frequency, and the turns of one key and of a warp's stride of TW blocks; pairs
   // past rk (they share a 16-dim step with rotated ones) keep still
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
     const int b_lo = a.cut ? (x - before) % blocks : 0;
     const int b_hi = a.cut ? min(blocks, x_end - x + b_lo) : blocks;
     const int kvh = u % a.c.hkv, row0 = u / a.c.hkv * kPR;
-    const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0, len = __ldg(a.lens + b);
+    const int tok0 = fresh(a.cu_q + b), n = fresh(a.cu_q + b + 1) - tok0, len = fresh(a.lens + b);
     const int rows = min(kPR, n * a.group - row0);
     const int first = keys_first(a, len, 0), end = len + n, blk0 = first / kPB;
     if (a.cut && b_lo == 0 && b_hi < blocks && tw == 0 && lane == 0)
@@ -360,8 +360,8 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
         const int j = 2 * lane + 64 * i;
         w0[i] = w1[i] = 0u;
         if (j < HALF) {
-          w0[i] = __ldg(reinterpret_cast<const uint32_t*>(src + j));
-          w1[i] = __ldg(reinterpret_cast<const uint32_t*>(src + HALF + j));
+          w0[i] = fresh(reinterpret_cast<const uint32_t*>(src + j));
+          w1[i] = fresh(reinterpret_cast<const uint32_t*>(src + HALF + j));
         }
       }
       uint32_t top = 0;

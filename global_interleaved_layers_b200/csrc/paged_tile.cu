@@ -314,9 +314,9 @@ struct TileWalk {
     p.b = b;
     p.kvh = u % hkv;
     p.row0 = u / hkv * a.unit_rows;
-    p.tok0 = __ldg(a.cu_q + b);
-    const int n = __ldg(a.cu_q + b + 1) - p.tok0;
-    p.len = __ldg(a.lens + b);
+    p.tok0 = fresh(a.cu_q + b);
+    const int n = fresh(a.cu_q + b + 1) - p.tok0;
+    p.len = fresh(a.lens + b);
     p.rows = min(a.unit_rows, n * a.group - p.row0);
     p.first = keys_first(a, p.len, 0);
     p.end = p.len + n;
@@ -425,8 +425,8 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
   if (a.chunk_of == nullptr && blockIdx.x == 0)
 #pragma unroll 1
     for (int b = threadIdx.x; b < a.batch; b += kTThreads) {
-      const int tok0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - tok0;
-      if (n != 0 && !seq_ok(a, tok0, n, __ldg(a.lens + b))) atomicOr(&g_status, kStatusSeqlen);
+      const int tok0 = fresh(a.cu_q + b), n = fresh(a.cu_q + b + 1) - tok0;
+      if (n != 0 && !seq_ok(a, tok0, n, fresh(a.lens + b))) atomicOr(&g_status, kStatusSeqlen);
     }
   fence_proxy_async_smem();
   if (warp == 1) {
@@ -469,7 +469,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
       const int32_t* table = a.c.table + (size_t)p.b * a.c.max_blocks;
       // Whether some query sees this lane's box of tile kt, and its table entry, read a tile ahead
       auto seen = [&](int kt) { return lane < boxes && kt * KT + lane * box < p.end && kt * KT + (lane + 1) * box > p.first; };
-      auto entry = [&](int kt) { return seen(kt) ? __ldg(table + ((kt * KT + lane * box) >> a.c.page_shift)) : -1; };
+      auto entry = [&](int kt) { return seen(kt) ? fresh(table + ((kt * KT + lane * box) >> a.c.page_shift)) : -1; };
       int next = entry(p.kt0);
 #pragma unroll 1
       for (int lt = 0; lt < p.ntiles && ok; ++lt, ++t) {
@@ -780,8 +780,8 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
 #pragma unroll
         for (int i = 0; i < QI; ++i) {
           const bool get = have && 2 * lane + 64 * i < HALF;
-          w0[i] = get ? __ldg(reinterpret_cast<const uint32_t*>(src + 2 * lane + 64 * i)) : 0u;
-          w1[i] = get ? __ldg(reinterpret_cast<const uint32_t*>(src + HALF + 2 * lane + 64 * i)) : 0u;
+          w0[i] = get ? fresh(reinterpret_cast<const uint32_t*>(src + 2 * lane + 64 * i)) : 0u;
+          w1[i] = get ? fresh(reinterpret_cast<const uint32_t*>(src + HALF + 2 * lane + 64 * i)) : 0u;
         }
         if (have && tk != angle_tk) {
           angle_tk = tk;
@@ -1003,15 +1003,15 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
     int entry = -1;
     auto read_entry = [&](const TilePiece& w, int lt) {
       const int pos = (w.kt0 + lt) * KT + u;
-      entry = lt < w.ntiles && pos >= w.first && pos < w.end ? __ldg(a.c.table + (size_t)w.b * a.c.max_blocks + (pos >> a.c.page_shift)) : -1;
+      entry = lt < w.ntiles && pos >= w.first && pos < w.end ? fresh(a.c.table + (size_t)w.b * a.c.max_blocks + (pos >> a.c.page_shift)) : -1;
     };
     auto read_scales = [&](const TilePiece& w, int lt) {  // of tile lt, by its entry; and the next one's entry
       const int pos = (w.kt0 + lt) * KT + u;
       ks_next = vs_next = 1.f;
       if ((unsigned)entry < (unsigned)a.c.num_pages) {
         const size_t row = page_row(a.c, entry, w.kvh, pos & ((1 << a.c.page_shift) - 1));
-        ks_next = __ldg(a.c.k_scales + row);
-        if (!SAME) vs_next = __ldg(a.c.v_scales + row);
+        ks_next = fresh(a.c.k_scales + row);
+        if (!SAME) vs_next = fresh(a.c.v_scales + row);
       }
       read_entry(w, lt + TG);
     };
