@@ -297,12 +297,25 @@ def paged_cache(k_pages, v_pages, block_table, k_scales=None, v_scales=None) -> 
     return c
 
 
+def _device_of(device, *tensors):
+    """The device that a call's tensors have to be on: the handle's, else that of the first tensor
+    among the arguments; None when all of them are raw addresses."""
+    if device is None:
+        for x in tensors:
+            if x is not None and type(x) is not int:
+                return x.device
+    return device
+
+
 def _call(fn, where: str, device, stream, *args) -> None:
     """fn(*args, stream) with `device` (of the call's tensors, or None) current; by default the stream
-    is that device's current one."""
-    if device is None or device.type != "cuda":
+    is that device's current one. Tensors that are not on a CUDA device are refused here, after all
+    other checks: their addresses mean nothing to a kernel."""
+    if device is None:
         _check(fn(*args, _stream(stream)), where)
         return
+    if device.type != "cuda":
+        _refuse(where, f"tensors are on {device}, not on a CUDA device")
     import torch
     if torch.cuda.current_device() != device.index:
         with torch.cuda.device(device):
@@ -335,7 +348,7 @@ def gemma_attn_paged_append(p: GemmaAttnParams, cache: GemmaAttnPagedCache, new_
     """New rows into a paged cache: row cu_q[b] + i goes to position cache_seqlens[b] + i of sequence b."""
     import torch
     where = "gemma_attn_paged_append"
-    dev = _cache_fits(p, cache, batch, where)
+    dev = _device_of(_cache_fits(p, cache, batch, where), new_k, new_v, cu_q, cache_seqlens)
     shape = (total_q, p.num_kv_heads, p.head_dim)
     _call(_lib.gemma_attn_paged_append, where, dev, stream, ctypes.byref(p), ctypes.byref(cache),
           _tensor(new_k, where, "new_k", torch.bfloat16, shape, dev),
@@ -349,7 +362,7 @@ def gemma_attn_paged_gather(p: GemmaAttnParams, cache: GemmaAttnPagedCache, star
     """Rows read back: row cu_out[b] + i receives position starts[b] + i of sequence b (params' out_dtype)."""
     import torch
     where = "gemma_attn_paged_gather"
-    dev = _cache_fits(p, cache, batch, where)
+    dev = _device_of(_cache_fits(p, cache, batch, where), starts, cu_out, out_k, out_v)
     shape = (total_out, p.num_kv_heads, p.head_dim)
     dt = torch.float32 if p.out_dtype == OUT_F32 else torch.bfloat16
     _call(_lib.gemma_attn_paged_gather, where, dev, stream, ctypes.byref(p), ctypes.byref(cache),
@@ -373,7 +386,7 @@ def gemma_attn_paged_attend(p: GemmaAttnParams, cache: GemmaAttnPagedCache, q, c
     """Attention of a chunk of new tokens over a paged cache that already holds their rows."""
     import torch
     where = "gemma_attn_paged_attend"
-    dev = _cache_fits(p, cache, batch, where)
+    dev = _device_of(_cache_fits(p, cache, batch, where), q, cu_q, cache_seqlens, out, lse, workspace)
     shape = (total_q, p.num_q_heads, p.head_dim)
     ws = workspace
     if ws is not None and type(ws) is not int:
