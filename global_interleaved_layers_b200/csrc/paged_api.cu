@@ -40,6 +40,11 @@ int paged_prepare(const gemma_attn_params* p, const gemma_attn_paged_cache* c, P
   return GEMMA_ATTN_OK;
 }
 
+// Lengths, prefixes and log-sum-exps are read and written 4 bytes at a time.
+bool aligned4(const void* x, const void* y, const void* z = nullptr) {
+  return (((uintptr_t)x | (uintptr_t)y | (uintptr_t)z) & 3u) == 0;
+}
+
 int launched(cudaError_t e, int launches) {
   if (e != cudaSuccess) return GEMMA_ATTN_ERR_LAUNCH;
   set_launch_count(launches);
@@ -204,7 +209,7 @@ int gemma_attn_paged_append(const gemma_attn_params* params, const gemma_attn_pa
   if (batch > 65535) return GEMMA_ATTN_ERR_UNSUPPORTED;
   if (total_q == 0) return GEMMA_ATTN_OK;
   if (!new_k || (new_v != nullptr) != (a.c.v != nullptr)) return GEMMA_ATTN_ERR_INVALID_ARG;
-  if (((uintptr_t)new_k | (uintptr_t)new_v) & 15u) return GEMMA_ATTN_ERR_MISALIGNED;
+  if (((uintptr_t)new_k | (uintptr_t)new_v) & 15u || !aligned4(cu_q, cache_seqlens)) return GEMMA_ATTN_ERR_MISALIGNED;
   a.new_k = static_cast<const uint16_t*>(new_k);
   a.new_v = static_cast<const uint16_t*>(new_v);
   a.cu_q = cu_q;
@@ -233,7 +238,7 @@ int gemma_attn_paged_gather(const gemma_attn_params* params, const gemma_attn_pa
   if (batch > 65535) return GEMMA_ATTN_ERR_UNSUPPORTED;
   if (total_out == 0) return GEMMA_ATTN_OK;
   if (!out_k || (out_v != nullptr) != (a.c.v != nullptr)) return GEMMA_ATTN_ERR_INVALID_ARG;
-  if (((uintptr_t)out_k | (uintptr_t)out_v) & 15u) return GEMMA_ATTN_ERR_MISALIGNED;
+  if (((uintptr_t)out_k | (uintptr_t)out_v) & 15u || !aligned4(starts, cu_out)) return GEMMA_ATTN_ERR_MISALIGNED;
   a.starts = starts;
   a.cu_out = cu_out;
   a.out_k = out_k;
@@ -278,7 +283,7 @@ int gemma_attn_paged_attend(const gemma_attn_params* params, const gemma_attn_pa
   if (!cu_q || !cache_seqlens) return GEMMA_ATTN_ERR_INVALID_ARG;
   if (total_q == 0 || max_q == 0) return GEMMA_ATTN_OK;
   if (!q || !out) return GEMMA_ATTN_ERR_INVALID_ARG;
-  if (((uintptr_t)q | (uintptr_t)out) & 15u) return GEMMA_ATTN_ERR_MISALIGNED;
+  if (((uintptr_t)q | (uintptr_t)out) & 15u || !aligned4(cu_q, cache_seqlens, lse)) return GEMMA_ATTN_ERR_MISALIGNED;
   if (plan.total > 0 && (!workspace || workspace_bytes < plan.total)) return GEMMA_ATTN_ERR_WORKSPACE;
   if ((uintptr_t)workspace & 255u) return GEMMA_ATTN_ERR_MISALIGNED;
   a.q = static_cast<const uint16_t*>(q);
