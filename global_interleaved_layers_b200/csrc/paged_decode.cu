@@ -25,8 +25,11 @@
 // power of two that brings their largest magnitude into [2^14, 2^15): a bf16 element keeps
 // all its bits down to 2^-21 of the row's largest, and what is lost below is under 2^-39 of
 // it. A key's scale multiplies its scores in fp32. A value's scale 2^k is folded into its
-// weight: with e = s + k (log2 units), P = 2^(e - max e) is what multiplies the codes, so the
-// largest weight is near 1 whatever the scales, and the softmax sum keeps a running maximum of s of its own.
+// weight: with e = s + k (log2 units), P = 2^(e - max e + 7) is what multiplies the codes, so the
+// largest weight is 2^7 to 2^15 whatever the scales, and the softmax sum keeps a running maximum of s of
+// its own. fp16's fixed step at the bottom, 2^-24, then leaves a weight off by at most 2^-32 of the
+// row's largest (2^-11 of itself above that): a flat tail of a million keys by 2^-12 of the output
+// altogether. With the largest weight at 1, a quarter of a million keys at 2^-25 of it were lost, 1 percent.
 //
 // Bound: HBM (each visible row is read once). 16 keys of 512 dims are 16 KB (8 KB in e4m3)
 // against 64 mma.sync and, for GLOBAL, the rotation of 16 x r pairs.
@@ -42,6 +45,8 @@ constexpr int kPB = 16;            // keys per block
 constexpr int kPR = 8;             // rows per group
 constexpr int kPHeader = 1408;     // mbarriers [2][warps][4], abort flag, run length, row scales, merge maxima and sums
 constexpr int kPMaxSmem = 227 * 1024;
+constexpr float kRaise = 8.f;      // a running maximum moves when it is passed by more than this (log2 units)
+constexpr float kTop16 = 7.f;      // fp16 weights: 2^7 at the running maximum, 2^(7 + 8) < 65504 at most
 
 // D(16x8 f32) += A(16x16 f16, row) * B(16x8 f16, col)
 __device__ __forceinline__ void mma_16816_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -629,10 +634,10 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
           oacc[mt][3] *= al[1];
         }
       };
-      // a running maximum moves only when it is passed by more than 8 (log2 units): weights stay
-      // below 2^8, and the accumulators are rarely touched; the decision is warp-uniform
+      // a running maximum moves only when it is passed by more than kRaise: weights stay bounded, and
+      // the accumulators are rarely touched; the decision is warp-uniform
       if constexpr (!E4M3) {
-        if (__any_sync(0xffffffffu, mx[0] > m_run[0] + 8.f || mx[1] > m_run[1] + 8.f)) {
+        if (__any_sync(0xffffffffu, mx[0] > m_run[0] + kRaise || mx[1] > m_run[1] + kRaise)) {
           float al[2];
   #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -664,7 +669,7 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
           }
         }
         row_max(mxv);
-        if (__any_sync(0xffffffffu, mx[0] > m_run[0] + 8.f || mx[1] > m_run[1] + 8.f)) {
+        if (__any_sync(0xffffffffu, mx[0] > m_run[0] + kRaise || mx[1] > m_run[1] + kRaise)) {
   #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float mn = fmaxf(m_run[h], mx[h]);
@@ -672,7 +677,7 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
             m_run[h] = mn;
           }
         }
-        if (__any_sync(0xffffffffu, mxv[0] > mv_run[0] + 8.f || mxv[1] > mv_run[1] + 8.f)) {
+        if (__any_sync(0xffffffffu, mxv[0] > mv_run[0] + kRaise || mxv[1] > mv_run[1] + kRaise)) {
           float al[2];
   #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -686,8 +691,8 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
         for (int h = 0; h < 2; ++h) {
           const float ms = m_run[h] == -INFINITY ? 0.f : m_run[h], mv = mv_run[h] == -INFINITY ? 0.f : mv_run[h];
           l_run[h] += exp2f(sacc[h] - ms) + exp2f(sacc[2 + h] - ms);
-          ev[h] = exp2f(ev[h] - mv);
-          ev[2 + h] = exp2f(ev[2 + h] - mv);
+          ev[h] = exp2f((ev[h] - mv) + kTop16);
+          ev[2 + h] = exp2f((ev[2 + h] - mv) + kTop16);
         }
         p01 = pack_f16x2(ev[0], ev[1]);
         p23 = pack_f16x2(ev[2], ev[3]);
@@ -766,7 +771,7 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
       float M, Lsum;
       merged(2 * t + h, M, Lsum);
       const float mo = E4M3 ? mv_run[h] : m_run[h];  // the weights' own reference
-      const float fac = Lsum != Lsum ? Lsum : Lsum > 0.f && mo != -INFINITY ? exp2f(mo - M) / Lsum : 0.f;
+      const float fac = Lsum != Lsum ? Lsum : Lsum > 0.f && mo != -INFINITY ? exp2f((mo - M) - (E4M3 ? kTop16 : 0.f)) / Lsum : 0.f;
       float* dst = red + (2 * t + h) * RED;
 #pragma unroll
       for (int mt = 0; mt < NKS; ++mt) {

@@ -29,9 +29,9 @@ def ints(v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
 
 
-def check_sink(kind, d, dtype, tokens, batch, n, sink, spread, top=20.0):
+def check_sink(kind, d, dtype, tokens, batch, n, sink, spread, low=10.0, top=20.0):
     """`batch` sequences over the same n cached rows, 8 heads of `tokens` new tokens each: row i has
-    its sink's weight 2^10 to 2^top times the tail's, whose logits are equal or have a deviation of
+    its sink's weight 2^low to 2^top times the tail's, whose logits are equal or have a deviation of
     `spread`. Values have the mean 0.5, the sink's -0.5."""
     page, heads = 256, 8
     gen = torch.Generator(device="cuda").manual_seed(d + n + tokens)
@@ -61,7 +61,7 @@ def check_sink(kind, d, dtype, tokens, batch, n, sink, spread, top=20.0):
     table = torch.arange(n // page, dtype=torch.int32, device="cuda").expand(batch, -1).contiguous()
     cache = G.paged_cache(pools[0], pools[1] if local else None, table, k_scales=scales[0],
                           v_scales=scales[1] if local else None)
-    ratio = torch.linspace(10, top, tokens * heads, device="cuda")
+    ratio = torch.linspace(low, top, tokens * heads, device="cuda")
     q = torch.zeros(tokens * heads, d, device="cuda")
     q[:, 1:] = torch.randn(tokens * heads, d - 1, generator=gen, device="cuda") * spread
     q[:, 0] = ratio * math.log(2) / (4 * par.softmax_scale)
@@ -104,6 +104,15 @@ def test_a_sink_and_a_long_tail(kind, d, dtype, tokens, spread, batch):
 @pytest.mark.parametrize("kind,d", [(G.GLOBAL, 512), (G.LOCAL, 128)])
 def test_a_sink_and_a_very_long_tail(kind, d, tokens, spread):
     check_sink(kind, d, "e4m3", tokens, 148, 131072, 20000 if tokens == 1 else 5, spread)
+
+
+# 64 dims: 1184 sequences, each with a warp of its own, or 3 that are cut
+@pytest.mark.parametrize("batch", [1184, 3])
+@pytest.mark.parametrize("spread", [0.0, 0.45])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kind", [G.GLOBAL, G.LOCAL])
+def test_a_sink_and_a_quarter_of_a_million_keys_of_64_dims(kind, dtype, spread, batch):
+    check_sink(kind, 64, dtype, 1, batch, 262144, 70, spread, low=20.0, top=25.5)
 
 
 @pytest.mark.parametrize("nq", [1, 4, 20])
