@@ -24,7 +24,7 @@
 // and the products run in fp16 with fp32 accumulation. Query rows enter in fp16 scaled by a
 // power of two that brings their largest magnitude into [2^14, 2^15): a bf16 element keeps
 // all its bits down to 2^-21 of the row's largest, and what is lost below is under 2^-39 of
-// it. A key's scale multiplies its scores in fp32. A value's scale 2^k is folded into its
+// it; a rotated one is rounded once, from fp32, by at most 2^-11 of itself. A key's scale multiplies its scores in fp32. A value's scale 2^k is folded into its
 // weight: with e = s + k (log2 units), P = 2^(e - max e + 7) is what multiplies the codes, so the
 // largest weight is 2^7 to 2^15 whatever the scales, and the softmax sum keeps a running maximum of s of
 // its own. fp16's fixed step at the bottom, 2^-24, then leaves a weight off by at most 2^-32 of the
@@ -369,24 +369,27 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
           w1[i] = fresh(reinterpret_cast<const uint32_t*>(src + HALF + j));
         }
       }
+      // x0, x1: the row's elements in fp32, rotated. They are rounded once: to bf16, or scaled to fp16
+      float x0[QI][2], x1[QI][2];
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < QI; ++i) {
         const int j = 2 * lane + 64 * i;
-        if (j < r) {
-          float c[2], s[2];
+        x0[i][0] = __uint_as_float(w0[i] << 16);
+        x0[i][1] = __uint_as_float(w0[i] & 0xFFFF0000u);
+        x1[i][0] = __uint_as_float(w1[i] << 16);
+        x1[i][1] = __uint_as_float(w1[i] & 0xFFFF0000u);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            c[e] = 1.f;
-            s[e] = 0.f;
-            if (j + e < r) rope_cos_sin((double)(len + tk), itf[j + e], &c[e], &s[e]);
+        for (int e = 0; e < 2; ++e) {
+          if (j + e < r) {
+            float c, s;
+            rope_cos_sin((double)(len + tk), itf[j + e], &c, &s);
+            const float y0 = x0[i][e] * c - x1[i][e] * s;
+            x1[i][e] = x0[i][e] * s + x1[i][e] * c;
+            x0[i][e] = y0;
           }
-          const float x00 = __uint_as_float(w0[i] << 16), x01 = __uint_as_float(w0[i] & 0xFFFF0000u);
-          const float x10 = __uint_as_float(w1[i] << 16), x11 = __uint_as_float(w1[i] & 0xFFFF0000u);
-          w0[i] = pack_bf16x2(x00 * c[0] - x10 * s[0], x01 * c[1] - x11 * s[1]);
-          w1[i] = pack_bf16x2(x00 * s[0] + x10 * c[0], x01 * s[1] + x11 * c[1]);
+          if (E4M3) top = max(top, max(__float_as_uint(x0[i][e]) & 0x7FFFFFFFu, __float_as_uint(x1[i][e]) & 0x7FFFFFFFu));
         }
-        top = max(max(top, max((w0[i] & 0x7FFFu) << 16, w0[i] & 0x7FFF0000u)), max((w1[i] & 0x7FFFu) << 16, w1[i] & 0x7FFF0000u));
       }
       if constexpr (E4M3) {
 #pragma unroll
@@ -398,10 +401,16 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
         const float up = __uint_as_float((uint32_t)(127 + k) << 23);
 #pragma unroll
         for (int i = 0; i < QI; ++i) {
-          w0[i] = pack_f16x2(__uint_as_float(w0[i] << 16) * up, __uint_as_float(w0[i] & 0xFFFF0000u) * up);
-          w1[i] = pack_f16x2(__uint_as_float(w1[i] << 16) * up, __uint_as_float(w1[i] & 0xFFFF0000u) * up);
+          w0[i] = pack_f16x2(x0[i][0] * up, x0[i][1] * up);
+          w1[i] = pack_f16x2(x1[i][0] * up, x1[i][1] * up);
         }
         if (lane == 0) s_qs[row] = __uint_as_float((uint32_t)(127 - k) << 23);
+      } else {
+#pragma unroll
+        for (int i = 0; i < QI; ++i) {
+          w0[i] = pack_bf16x2(x0[i][0], x0[i][1]);
+          w1[i] = pack_bf16x2(x1[i][0], x1[i][1]);
+        }
       }
 #pragma unroll
       for (int i = 0; i < QI; ++i) {
