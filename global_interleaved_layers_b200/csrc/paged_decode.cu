@@ -114,13 +114,14 @@ __host__ __device__ inline PagedLayout paged_layout(const PagedRowsShape& f, boo
 }
 
 // The first form that fits in shared memory: eight warps with as many stages as fit, then four.
+// 64 dims always have eight with four stages (of values too, where they are separate), 256 dims
+// eight with one to four; what is left are K=V rows of 512 dims and many rotated pairs.
 template <int D, bool E4M3>
 bool paged_rows_stages(PagedRowsShape* f, bool kv_same, int r) {
-  static const int forms[][3] = {{8, 4, 4}, {8, 3, 3}, {8, 3, 2}, {8, 2, 2}, {8, 2, 1}, {8, 1, 1}, {4, 2, 1}, {4, 1, 1}};
+  static const int forms[][2] = {{8, 4}, {8, 3}, {8, 2}, {8, 1}, {4, 2}};
   for (const auto& x : forms) {
     f->nw = x[0];
-    f->nsk = x[1];
-    f->nsv = x[2];
+    f->nsk = f->nsv = x[1];
     if (paged_layout<D, E4M3>(*f, kv_same, r).total <= (uint32_t)kPMaxSmem) return true;
   }
   return false;
@@ -971,7 +972,9 @@ static cudaError_t launch_paged_rows_t(PagedAttendArgs a, const PagedRowsShape& 
 template <int D, bool E4M3>
 static cudaError_t launch_paged_rows_d(const PagedAttendArgs& a, PagedRowsShape f, long long units, cudaStream_t stream) {
   if (!paged_rows_stages<D, E4M3>(&f, a.c.v == nullptr, a.r)) return cudaErrorInvalidValue;
-  return f.nw == 8 ? launch_paged_rows_t<D, E4M3, 8>(a, f, units, stream) : launch_paged_rows_t<D, E4M3, 4>(a, f, units, stream);
+  if constexpr (D == 512)
+    if (f.nw == 4) return launch_paged_rows_t<D, E4M3, 4>(a, f, units, stream);
+  return f.nw == 8 ? launch_paged_rows_t<D, E4M3, 8>(a, f, units, stream) : cudaErrorInvalidValue;
 }
 
 cudaError_t launch_paged_rows(const PagedAttendArgs& a, const PagedRowsShape& f, bool e4m3, cudaStream_t stream) {
