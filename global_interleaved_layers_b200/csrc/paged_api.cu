@@ -51,7 +51,12 @@ int launched(cudaError_t e, int launches) {
   return GEMMA_ATTN_OK;
 }
 
-// Rows per KV head up to which a sequence takes the row-group kernel.
+// Rows per KV head up to which a sequence takes the kernels of short sequences; with more it is a
+// chunk. Up to 40 rows they are one unit there (paged_rows_shape), up to 80 two, each with all the
+// keys read. Measured, us, with the border at 40, 64 and 128 rows: 16 sequences of 1k to 32k keys, K=V of
+// 512 dims, 64 rows: chunks 324, units 218 in e4m3, 250 and 208 in bf16; 80 rows: 332 and 220, 258 and
+// 210; 128 rows (four units): 344 and 382, 270 and 370. On a window of 1,024 with 256 dims, where a
+// chunk's fixed launches weigh less than second units: 60 rows 125 and 171, 80 rows 132 and 173.
 constexpr int kChunkMinRows = 64;
 
 // How an attend call's work is cut, and what of the workspace each part takes (byte offsets).

@@ -908,9 +908,16 @@ cudaError_t launch_paged_merge(const PagedAttendArgs& a, cudaStream_t stream) {
 //   rounds to 80 percent.
 //   The tensor-core kernel (paged_tile.cu) takes what it can: head dims from 128, at most 64
 //   rotated pairs of K=V keys (128 dims have no more). Measured, tensor-core kernel against this
-//   file's: one sequence of 100 keys, 256 dims, 16 against 18 us; 64 sequences on a window of
-//   1,024 in e4m3, 137 against 229; 8 of 32k keys, 512 dims, 188 against 260; five tokens each of 16
-//   sequences against up to 32k keys in e4m3, 137 against 559.
+//   file's, in turn on one card: 64 sequences on a window of 1,024 in e4m3, 136 against 236 us; 8 of 32k
+//   keys, 512 dims, 187 against 279; five tokens each of 16 sequences against up to 32k keys in e4m3,
+//   128 against 591; one sequence of 100 keys, 256 dims, 12.5 against 10.3, the one place seen where it
+//   loses (TMEM, tensor maps and five roles to start for one tile).
+//   Its units: 8 rows where all sequences have no more, 40 otherwise: five tokens (four drafted) of eight
+//   heads are one unit. Measured at 16 sequences of 1k to 32k keys, K=V of 512 dims, units of 40
+//   against units of 8, us: 16 rows 128 against 101 in e4m3, 126 against 128 in bf16; 24 rows 130
+//   against 136, 130 against 177; 40 rows 136 against 212, 132 against 280; on a window of 1,024 with
+//   256 dims, 16 rows 95 against 132. (8 rows in a unit of 8 take 67 and 87.)
+//   More than 64 rows are a chunk (paged_api.cu).
 PagedRowsShape paged_rows_shape(int head_dim, bool local, int rotated, int batch, int hkv, int rows, long long keys) {
   PagedRowsShape f{};
   if (head_dim >= 128 && (local || rotated <= 64)) {

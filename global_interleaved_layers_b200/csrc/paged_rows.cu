@@ -18,7 +18,8 @@
 // the group. Whole warps are filled for every head dim.
 // Measured (cold L2): append and gather of a decode step, 64 sequences x 16 KV heads x 256 dims, K
 // and V, e4m3: 8 and 6 us; of 1,000 to 8,191 tokens of six sequences, K=V of 4 x 512: 20 and 17 us
-// (4.6 and 5.4 TB/s); gather of three whole sequences, 53k tokens of 16 x 256, 205 us (5.5 TB/s).
+// (4.6 and 5.4 TB/s); gather of three whole sequences, 53k tokens of 16 x 256, 206 to 213 us by the card
+// (5.3 to 5.5 TB/s).
 // A head at a time (the loads of one in flight) the last two took 43 and 233 us.
 #include "paged.h"
 

@@ -22,10 +22,10 @@
 // of the output; without the factor of 16, 9), so a weight's lo is rounded with a dither: half a
 // step times a number in [-1, 1) that goes through the key positions by the golden ratio. It leaves
 // a weight off by up to 2^-13, without bias, and neighbours' errors cancel (the same tail: 1.4e-4 by
-// arithmetic, 6e-4 measured, of fp32's own additions; weights that are zero stay zero). N is twice the rows, and with N's granularity of 16 the second
-// half of 8 rows is free. The rotated dims are fp16 (codes turned in fp32, one
-// rounding of 2^-11) in kind::f16 MMAs on hi's accumulators. A key's scale multiplies its
-// scores; a value's scale 2^k is folded into its weight: with e = s + k in log2 units, the
+// arithmetic, 6e-4 measured, of fp32's own additions; weights that are zero stay zero). N is twice
+// the rows, and with N's granularity of 16 the second half of 8 rows is free. The rotated dims are
+// fp16 (codes turned in fp32, one rounding of 2^-11) in kind::f16 MMAs on hi's accumulators. A key's
+// scale multiplies its scores; a value's scale 2^k is folded into its weight: with e = s + k in log2 units, the
 // weight is 2^(e - mv + 7) for a running mv near max e, and the softmax sum takes 2^(s - m) with
 // an m of its own, so scales of any size only move exponents.
 //
@@ -48,7 +48,7 @@
 // Every wait is bounded: one that runs out records a timeout and the CTA unwinds.
 //
 // Bound: HBM, each visible row read once. Measured (cold L2): 8 sequences of 30k to 32k keys, 512
-// dims, bf16, 188 us with the join (5.4 TB/s; the loads' share of HBM is 24 B a cycle and SM,
+// dims, bf16, 185 to 198 us by the card, with the join (5.1 to 5.5 TB/s; the loads' share of HBM is 24 B a cycle and SM,
 // a 64 KB tile takes 3,000 cycles of the 2,700 that allows); 64 sequences on a window of 1,024,
 // 256 dims, e4m3, 136 us (3.7 TB/s: a unit is nine tiles, and its first scores and its output
 // leave gaps); 40 rows of 16 sequences against 1k to 32k keys, 512 dims, e4m3, 128 us: there the ring
