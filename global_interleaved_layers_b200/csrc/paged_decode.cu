@@ -665,20 +665,25 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
         l_run[0] += __uint_as_float(p01 << 16) + __uint_as_float(p23 << 16);
         l_run[1] += __uint_as_float(p01 & 0xFFFF0000u) + __uint_as_float(p23 & 0xFFFF0000u);
       } else {
-        // log2 of the value scales (powers of two; NaN stays NaN)
-        float ev[4], mxv[2] = {-INFINITY, -INFINITY};
+        float ev[4], mxv[2], vs[2];
   #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float vs = kv_same ? ks[k] : scs[(nsk + sv) * 16 + g + 8 * k];
-          const float lv = vs == vs ? (float)((int)(__float_as_uint(vs) >> 23) - 127) : vs;
+        for (int k = 0; k < 2; ++k) vs[k] = kv_same ? ks[k] : scs[(nsk + sv) * 16 + g + 8 * k];
+        auto fold = [&]() {
+          mxv[0] = mxv[1] = -INFINITY;
   #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int e = 2 * k + h;
-            ev[e] = sacc[e] == -INFINITY ? -INFINITY : sacc[e] + lv;
-            mxv[h] = fmaxf(mxv[h], ev[e]);
+          for (int k = 0; k < 2; ++k) {
+            // log2 of the value scales (powers of two; NaN stays NaN)
+            const float lv = vs[k] == vs[k] ? (float)((int)(__float_as_uint(vs[k]) >> 23) - 127) : vs[k];
+  #pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int e = 2 * k + h;
+              ev[e] = sacc[e] == -INFINITY ? -INFINITY : sacc[e] + lv;
+              mxv[h] = fmaxf(mxv[h], ev[e]);
+            }
           }
-        }
-        row_max(mxv);
+          row_max(mxv);
+        };
+        fold();
         if (__any_sync(0xffffffffu, mx[0] > m_run[0] + kRaise || mx[1] > m_run[1] + kRaise)) {
   #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -688,6 +693,22 @@ __global__ void __launch_bounds__(NW * 32) paged_rows_kernel(PagedAttendArgs a, 
           }
         }
         if (__any_sync(0xffffffffu, mxv[0] > mv_run[0] + kRaise || mxv[1] > mv_run[1] + kRaise)) {
+          if (__any_sync(0xffffffffu, vs[0] == 1.f || vs[1] == 1.f)) {
+            // rows of zeros among them? The four lanes of a key look at a quarter of its row each.
+  #pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t any = 0;
+  #pragma unroll 1
+              for (int i = t; i < D / 16; i += 4) {
+                const uint4 w = *reinterpret_cast<const uint4*>(vd + (g + 8 * k) * RS + 16 * i);
+                any |= w.x | w.y | w.z | w.w;
+              }
+              any |= __shfl_xor_sync(0xffffffffu, any, 1);
+              any |= __shfl_xor_sync(0xffffffffu, any, 2);
+              if (vs[k] == 1.f && (any & 0x7F7F7F7Fu) == 0) vs[k] = kZeroRowScale;
+            }
+            fold();
+          }
           float al[2];
   #pragma unroll
           for (int h = 0; h < 2; ++h) {

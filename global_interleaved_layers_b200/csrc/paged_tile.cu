@@ -27,7 +27,7 @@
 // fp16 (codes turned in fp32, one rounding of 2^-11) in kind::f16 MMAs on hi's accumulators. A key's
 // scale multiplies its scores; a value's scale 2^k is folded into its weight: with e = s + k in log2 units, the
 // weight is 2^(e - mv + 7) for a running mv near max e, and the softmax sum takes 2^(s - m) with
-// an m of its own, so scales of any size only move exponents.
+// an m of its own, so scales of any size only move exponents (rows of zeros: kZeroRowScale).
 //
 // Work. A unit is up to NR rows of one (sequence, KV head) against all keys its sequence sees.
 // Units go round the CTAs, or the tiles of all units are laid end to end and cut into equal runs,
@@ -283,6 +283,18 @@ __device__ __noinline__ float2 turn_of(double pos, double inv_freq_turns) {
   float2 r;
   rope_cos_sin(pos, inv_freq_turns, &r.x, &r.y);
   return r;
+}
+
+// Whether the value row at position pos, whose table entry is known to be good, is one of zeros.
+__device__ __noinline__ bool zero_row(const PagedAttendArgs& a, const uint8_t* pool, const TilePiece& p, int pos) {
+  const int page = fresh(a.c.table + (size_t)p.b * a.c.max_blocks + (pos >> a.c.page_shift));
+  const uint4* row = reinterpret_cast<const uint4*>(pool + page_row(a.c, page, p.kvh, pos & ((1 << a.c.page_shift) - 1)) * a.c.d);
+#pragma unroll 1
+  for (int i = 0; i < a.c.d / 16; ++i) {
+    const uint4 w = fresh(row + i);
+    if ((w.x | w.y | w.z | w.w) & 0x7F7F7F7Fu) return false;
+  }
+  return true;
 }
 
 // The CTA's pieces in turn, by one warp: units team, team + teams, ..., or a run of the line of
@@ -999,7 +1011,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
     };
     // e4m3: this thread's key's scales are read a tile of its group ahead, the table entry that leads
     // to them two tiles ahead, past the ends of units too, so that no tile waits for either
-    float ks_next = 1.f, vs_next = 1.f;
+    float ks_next = kZeroRowScale, vs_next = kZeroRowScale;
     int entry = -1;
     auto read_entry = [&](const TilePiece& w, int lt) {
       const int pos = (w.kt0 + lt) * KT + u;
@@ -1007,7 +1019,7 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
     };
     auto read_scales = [&](const TilePiece& w, int lt) {  // of tile lt, by its entry; and the next one's entry
       const int pos = (w.kt0 + lt) * KT + u;
-      ks_next = vs_next = 1.f;
+      ks_next = vs_next = kZeroRowScale;   // of keys that are not there, too
       if ((unsigned)entry < (unsigned)a.c.num_pages) {
         const size_t row = page_row(a.c, entry, w.kvh, pos & ((1 << a.c.page_shift) - 1));
         ks_next = fresh(a.c.k_scales + row);
@@ -1097,6 +1109,10 @@ paged_tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
         if (vv.x | vv.y | vv.z | vv.w) {
           // the four warps agree on the tile's maxima and raise the references to them
           auto& red = hd->red[meets & 1u][half];
+          if constexpr (E4M3) {
+            if (vscale == 1.f && zero_row(a, SAME ? a.c.k : a.c.v, p, k0 + u)) lv = -126.f;  // log2 of kZeroRowScale
+            __syncwarp();
+          }
           {
             float y[H], z[H];
 #pragma unroll
