@@ -24,11 +24,12 @@
 // and the products run in fp16 with fp32 accumulation. Query rows enter in fp16 scaled by a
 // power of two that brings their largest magnitude into [2^14, 2^15): a bf16 element keeps
 // all its bits down to 2^-21 of the row's largest, and what is lost below is under 2^-39 of
-// it; a rotated one is rounded once, from fp32, by at most 2^-11 of itself. A key's scale multiplies its scores in fp32. A value's scale 2^k is folded into its
-// weight: with e = s + k (log2 units), P = 2^(e - max e + 7) is what multiplies the codes, so the
-// largest weight is 2^7 to 2^15 whatever the scales, and the softmax sum keeps a running maximum of s of
-// its own. fp16's fixed step at the bottom, 2^-24, then leaves a weight off by at most 2^-32 of the
-// row's largest (2^-11 of itself above that): a flat tail of a million keys by 2^-12 of the output
+// it; a rotated one is rounded once, from fp32, by at most 2^-11 of itself. A key's scale
+// multiplies its scores in fp32. A value's scale 2^k is folded into its weight: with e = s + k (log2
+// units), P = 2^(e - max e + 7) is what multiplies the codes, so the largest weight is 2^7 to 2^15
+// whatever the scales (rows of zeros: kZeroRowScale), and the softmax sum keeps a running maximum of
+// s of its own. fp16's fixed step at the bottom, 2^-24, then leaves a weight off by at most 2^-32 of
+// the row's largest (2^-11 of itself above that): a flat tail of a million keys by 2^-12 of the output
 // altogether. With the largest weight at 1, a quarter of a million keys at 2^-25 of it were lost, 1 percent.
 //
 // Bound: HBM (each visible row is read once). 16 keys of 512 dims are 16 KB (8 KB in e4m3)

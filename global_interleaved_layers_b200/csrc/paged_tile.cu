@@ -48,8 +48,8 @@
 // Every wait is bounded: one that runs out records a timeout and the CTA unwinds.
 //
 // Bound: HBM, each visible row read once. Measured (cold L2): 8 sequences of 30k to 32k keys, 512
-// dims, bf16, 185 to 198 us by the card, with the join (5.1 to 5.5 TB/s; the loads' share of HBM is 24 B a cycle and SM,
-// a 64 KB tile takes 3,000 cycles of the 2,700 that allows); 64 sequences on a window of 1,024,
+// dims, bf16, 185 to 198 us by the card, with the join (5.1 to 5.5 TB/s; the loads' share of HBM is
+// 24 B a cycle and SM, a 64 KB tile takes 3,000 cycles of the 2,700 that allows); 64 sequences on a window of 1,024,
 // 256 dims, e4m3, 136 us (3.7 TB/s: a unit is nine tiles, and its first scores and its output
 // leave gaps); 40 rows of 16 sequences against 1k to 32k keys, 512 dims, e4m3, 128 us: there the ring
 // holds not two tiles beside the query rows' and weights' two columns each, and a tile's chain
